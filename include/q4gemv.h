@@ -68,7 +68,8 @@ typedef enum {
     Q4_EUNSUPPORTED = -6,  /* M outside [1, 256], or the device is not sm_100 */
     Q4_ETIMEOUT = -7,      /* a bounded device-side wait gave up */
     Q4_EFAULTINJ = -8,     /* a host step failed on purpose (fault injection) */
-    Q4_ECONCURRENT = -9    /* kernels saw overlapping calls on one handle */
+    Q4_ECONCURRENT = -9,   /* kernels saw overlapping calls on one handle */
+    Q4_EINDEX = -10        /* a page, place or state slot in device memory is out of range */
 } q4gemv_status;
 
 /* Limits checked by validation.  Besides these, ceil(N/32) * (K/32) must be
@@ -429,8 +430,160 @@ Q4GEMV_API int q4gemv_run_stack_sharded(q4gemv_t h, const q4gemv_layer* layers_l
 Q4GEMV_API int q4gemv_run_noalloc(const void* W_packed, const void* x, void* y, int M,
                                   int64_t N, int64_t K, q4gemv_stream_t stream);
 
+/* ---- Token mixing: what a layer does between its QKV and O products.  The
+ * pages' trunk is a hybrid of attention layers and linear-attention layers
+ * (taozi.news page, section "支持模型与限制"; originshq.com page, section
+ * "Limitations and Open Questions") and gives no equations: the definitions
+ * below are the common ones.
+ *
+ * A call takes the new tokens of a ragged batch of sequences: `rows` rows in
+ * all, sequence s holding rows [start[s], start[s+1]) (device, n_seqs + 1
+ * non-decreasing entries; a sequence may have none), and for the cached forms
+ * len[s] (device, n_seqs entries), the tokens of sequence s in the cache with
+ * the new ones counted.  New token t of n of sequence s thus has the place
+ * len[s] - n + t.  Rows behind start[n_seqs] belong to no sequence: nothing
+ * reads or writes them.  start, len, page tables and slots are read by the
+ * kernels when they run, so a captured call follows later changes of them.
+ * What they hold is checked on the device, never trusted: an entry out of
+ * range is left out (each function says how) and the next q4gemv_sync_status
+ * returns Q4_EINDEX.
+ *
+ * Elements are binary16 or bfloat16 (`dtype`, the same for every 16-bit
+ * buffer of a call).  Strides are in elements; row strides of 16-bit buffers
+ * are multiples of 8, so that rows keep the 16-byte alignment of their base;
+ * the heads of a row lie one after the other.  Sums, softmax statistics and
+ * states are in 32 bits, outputs rounded once.  All functions are
+ * deterministic, may be captured into a graph from the first call on, and
+ * launch nothing for rows == 0 (linattn: for n_seqs == 0). */
+typedef enum { Q4GEMV_F16 = 0, Q4GEMV_BF16 = 1 } q4gemv_dtype;
+
+#define Q4GEMV_MAX_HEAD_DIM 256      /* head_dim, k_dim, v_dim: multiples of 8 up to this */
+#define Q4GEMV_MAX_HEADS 1024
+#define Q4GEMV_MAX_SEQS 65535
+#define Q4GEMV_MAX_ROWS (1 << 24)
+
+/* A paged cache of keys and values (a host struct of device pointers, kept by
+ * the caller).  Token t of sequence s is in page p = table[s * table_stride +
+ * t / page_size], its head h at element p * page_stride +
+ * (t % page_size) * token_stride + h * head_stride of both k and v.  Pages
+ * that several sequences share may be read by all of them; a page that a
+ * sequence appends to must be its own. */
+typedef struct {
+    void* k;                 /* 16-byte aligned */
+    void* v;
+    const int32_t* table;    /* [n_seqs][table_stride], pages of the pool */
+    int64_t n_pages;         /* pages of the pool: 0 <= entry < n_pages */
+    int64_t page_size;       /* tokens of a page, any count from 1 to 2^20 */
+    int64_t n_heads;         /* key and value heads */
+    int64_t head_dim;
+    int64_t page_stride, token_stride, head_stride;   /* multiples of 8 */
+    int64_t table_stride, table_cols;   /* between rows; entries of a row */
+    int dtype;               /* q4gemv_dtype */
+} q4gemv_kv;
+
+/* Rotation of queries and keys by their positions.  The first `rot` (even)
+ * elements of a head are rot/2 pairs: elements (f, f + rot/2) in the half
+ * layout, (2f, 2f + 1) in the interleaved one; the rest passes.  Pair f of a
+ * token at position p turns by p * freqs[f] radians: (a cos - b sin,
+ * b cos + a sin) * amp.  Angles are taken in 64 bits. */
+typedef struct {
+    const double* freqs;     /* device, rot/2 entries (q4gemv_rope_freqs) */
+    int rot;                 /* 0: no rotation */
+    int interleaved;
+    float amp;               /* factor of cos and sin; 1 for none */
+} q4gemv_rope;
+
+enum {
+    Q4GEMV_ROPE_PLAIN = 0,      /* base^(-2f/rot) */
+    Q4GEMV_ROPE_LINEAR = 1,     /* that / factor: positions interpolated */
+    Q4GEMV_ROPE_BY_PARTS = 2    /* by the turns T that the pair takes in `trained` tokens:
+                                 * under `lo` turns / factor, over `hi` unchanged, between
+                                 * them mixed linearly in T */
+};
+
+/* Writes the rot/2 angular speeds of a rotation to `freqs` (HOST memory;
+ * host-only, no device access).  factor, trained, lo and hi are used by the
+ * scaled kinds only.  Q4_EINVAL for a null pointer, an unknown kind, base <= 0,
+ * factor < 1, trained <= 0, lo >= hi or a value that is not finite; Q4_ESHAPE
+ * for rot odd or outside [0, Q4GEMV_MAX_HEAD_DIM]. */
+Q4GEMV_API int q4gemv_rope_freqs(int kind, int rot, double base, double factor, double trained,
+                                 double lo, double hi, double* freqs);
+
+/* Appends the new tokens' keys and values to the cache, keys rotated, and
+ * rotates their queries.
+ *   pos   : device, [rows] rotation positions, or NULL: the places
+ *   rope  : host struct, or NULL: no rotation
+ *   q     : device, [rows][q_heads][head_dim], rows q_stride apart, or NULL
+ *           (then q_out is not used): the queries
+ *   k, v  : device, [rows][n_heads][head_dim]
+ *   q_out : device, rows q_out_stride apart; may be q (same stride), else it
+ *           must not overlap the inputs
+ * q, k and v may be slices of one row of the QKV product.  A row whose place
+ * is negative, past the table's columns or in a page outside the pool is not
+ * stored (Q4_EINDEX); its queries are rotated all the same. */
+Q4GEMV_API int q4gemv_kv_append(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_seqs,
+                                const int32_t* start, const int32_t* len, const int32_t* pos,
+                                const q4gemv_rope* rope, const void* q, int64_t q_stride,
+                                int64_t q_heads, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, void* q_out, int64_t q_out_stride,
+                                q4gemv_stream_t stream);
+
+/* Attention of the new tokens over the cache (which holds their own keys and
+ * values already):
+ *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale q.k_j),
+ * j over the tokens that the new token at place p sees: j <= p if `causal`,
+ * else every j < len[s]; with window > 0 only j > p - window.  Query head h
+ * reads key head h / (q_heads / n_heads).  A row that sees no token (or whose
+ * scores are all -Inf) gets zeros.  What a row does not see cannot reach it,
+ * whatever it holds: tokens behind len[s] or behind the row's place, and
+ * uninitialised parts of pages, may hold NaN.  Tokens in a page outside the
+ * pool are left out (Q4_EINDEX).
+ *   q     : device, [rows][q_heads][head_dim], rows q_stride apart
+ *   out   : device, the same shape, rows out_stride apart; must not overlap
+ *           q or the cache
+ *   max_new : the most new tokens of a sequence, as far as the caller knows
+ *           (1 <= max_new): it chooses the kernel, and results are right
+ *           whatever it says */
+Q4GEMV_API int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_seqs,
+                                 const int32_t* start, const int32_t* len, int64_t max_new,
+                                 const void* q, int64_t q_stride, int64_t q_heads, void* out,
+                                 int64_t out_stride, float scale, int causal, int64_t window,
+                                 q4gemv_stream_t stream);
+
+/* Linear attention with a decay for each head (a host struct of arguments):
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   out_t = scale S_t^T q_t,
+ * S the head's [k_dim][v_dim] state.  Value head h goes with query and key
+ * head h / (v_heads / qk_heads). */
+typedef struct {
+    const void* q;           /* [rows][qk_heads][k_dim], rows q_stride apart */
+    const void* k;           /* the same shape, rows k_stride apart */
+    const void* v;           /* [rows][v_heads][v_dim], rows v_stride apart */
+    const float* log_decay;  /* [rows][v_heads], rows decay_stride apart (any count, no
+                              * alignment beyond 4 bytes); decay_stride 0: one row, fixed
+                              * decays.  Entries <= 0 (-Inf clears the state) */
+    const float* state_in;   /* [n_slots][v_heads][k_dim][v_dim]; NULL: zeros */
+    float* state_out;        /* the same shape; may be state_in, else must not overlap it */
+    const int32_t* slots;    /* device, [n_seqs]: the state of sequence s, no two the
+                              * same; NULL: state s */
+    void* out;               /* [rows][v_heads][v_dim], rows out_stride apart; must not
+                              * overlap the inputs */
+    int64_t q_stride, k_stride, v_stride, decay_stride, out_stride;
+    int64_t n_slots, qk_heads, v_heads, k_dim, v_dim;
+    float scale;
+    int dtype;               /* q4gemv_dtype of q, k, v and out */
+} q4gemv_linattn_args;
+
+/* Runs the new tokens of every sequence through its state: reads state_in,
+ * writes state_out (of the sequences' slots only; a sequence without new
+ * tokens copies its state).  A sequence whose slot is outside [0, n_slots) is
+ * left out, its rows unwritten (Q4_EINDEX).  max_new as in
+ * q4gemv_attn_paged. */
+Q4GEMV_API int q4gemv_linattn(q4gemv_t h, const q4gemv_linattn_args* args, int64_t rows,
+                              int64_t n_seqs, const int32_t* start, int64_t max_new,
+                              q4gemv_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the handle's device error
- * word: Q4_OK, Q4_ETIMEOUT, Q4_ECONCURRENT, or Q4_ECUDA if an earlier
+ * word: Q4_OK, Q4_ETIMEOUT, Q4_ECONCURRENT, Q4_EINDEX, or Q4_ECUDA if an earlier
  * asynchronous error is pending on the device. */
 Q4GEMV_API int q4gemv_sync_status(q4gemv_t h, q4gemv_stream_t stream);
 

@@ -25,8 +25,11 @@ Q4_EUNSUPPORTED = -6
 Q4_ETIMEOUT = -7
 Q4_EFAULTINJ = -8
 Q4_ECONCURRENT = -9
+Q4_EINDEX = -10
 MAX_M = 256        # vectors per q4gemv_run call
 MAX_M_GEMV = 16    # above this, the tensor-core GEMM path
+F16, BF16 = 0, 1   # q4gemv_dtype
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BY_PARTS = 0, 1, 2
 
 
 class Q4Error(RuntimeError):
@@ -40,13 +43,39 @@ class q4gemv_layer(ctypes.Structure):
                 ("gate_up", ctypes.c_void_p), ("down", ctypes.c_void_p)]
 
 
+class q4gemv_kv(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("n_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+                ("table_cols", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class q4gemv_rope(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("amp", ctypes.c_float)]
+
+
+class q4gemv_linattn_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("log_decay", ctypes.c_void_p), ("state_in", ctypes.c_void_p),
+                ("state_out", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("decay_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("n_slots", ctypes.c_int64),
+                ("qk_heads", ctypes.c_int64), ("v_heads", ctypes.c_int64),
+                ("k_dim", ctypes.c_int64), ("v_dim", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
 def _load_library():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
             f"{LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'` "
             "or `python q4_quantized_decode_b200/build_ext.py`")
     lib = ctypes.CDLL(LIB_PATH)
-    vp, i64, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    vp, i64, ci, dbl = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
     sigs = {
         "q4gemv_version": ([], ci),
         "q4gemv_create": ([ctypes.POINTER(vp), ci], ci),
@@ -82,6 +111,13 @@ def _load_library():
         "q4gemv_q8_0_repack": ([vp, vp, vp, i64, i64, vp], ci),
         "q4gemv_q8_0_validate": ([ci, i64, i64, vp, vp, vp], ci),
         "q4gemv_q8_0_run": ([vp, vp, vp, vp, ci, i64, i64, vp], ci),
+        "q4gemv_rope_freqs": ([ci, ci, dbl, dbl, dbl, dbl, dbl, ctypes.POINTER(dbl)], ci),
+        "q4gemv_kv_append": ([vp, ctypes.POINTER(q4gemv_kv), i64, i64, vp, vp, vp,
+                              ctypes.POINTER(q4gemv_rope), vp, i64, i64, vp, i64, vp, i64, vp, i64,
+                              vp], ci),
+        "q4gemv_attn_paged": ([vp, ctypes.POINTER(q4gemv_kv), i64, i64, vp, vp, i64, vp, i64, i64, vp,
+                               i64, ctypes.c_float, ci, i64, vp], ci),
+        "q4gemv_linattn": ([vp, ctypes.POINTER(q4gemv_linattn_args), i64, i64, vp, i64, vp], ci),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -235,6 +271,30 @@ def q4gemv_q8_0_run(h, W, x, y, M, N, K, stream) -> int:
     return _lib.q4gemv_q8_0_run(h, W, x, y, M, N, K, stream)
 
 
+def q4gemv_rope_freqs(kind: int, rot: int, base: float, factor: float = 1.0, trained: float = 0.0,
+                      lo: float = 0.0, hi: float = 0.0):
+    """(status, [rot/2 radians per position]) of a rotation (see the header)."""
+    buf = (ctypes.c_double * max(1, rot // 2))()
+    st = _lib.q4gemv_rope_freqs(kind, rot, base, factor, trained, lo, hi, buf)
+    return st, list(buf[:rot // 2]) if st == Q4_OK else []
+
+
+def q4gemv_kv_append(h, kv, rows, n_seqs, start, length, pos, rope, q, q_stride, q_heads, k, k_stride,
+                     v, v_stride, q_out, q_out_stride, stream) -> int:
+    return _lib.q4gemv_kv_append(h, kv, rows, n_seqs, start, length, pos, rope, q, q_stride, q_heads,
+                                 k, k_stride, v, v_stride, q_out, q_out_stride, stream)
+
+
+def q4gemv_attn_paged(h, kv, rows, n_seqs, start, length, max_new, q, q_stride, q_heads, out,
+                      out_stride, scale, causal, window, stream) -> int:
+    return _lib.q4gemv_attn_paged(h, kv, rows, n_seqs, start, length, max_new, q, q_stride, q_heads,
+                                  out, out_stride, scale, causal, window, stream)
+
+
+def q4gemv_linattn(h, args, rows, n_seqs, start, max_new, stream) -> int:
+    return _lib.q4gemv_linattn(h, args, rows, n_seqs, start, max_new, stream)
+
+
 def _ptr(t) -> int | None:
     if t is None:
         return None
@@ -246,6 +306,63 @@ def _stream(stream) -> int:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _dtype_code(t) -> int:
+    import torch
+    if t.dtype == torch.float16:
+        return F16
+    if t.dtype == torch.bfloat16:
+        return BF16
+    raise Q4Error(Q4_EINVAL, f"tensor of {t.dtype}: float16 or bfloat16 expected")
+
+
+def _heads(t, name: str, dtype, device, rows=None, heads=None, dim=None):
+    """Row stride of t [rows][heads][dim], its heads and elements packed in a row."""
+    if t.dtype != dtype or t.device != device:
+        raise Q4Error(Q4_EINVAL, f"{name}: {t.dtype} on {t.device}, {dtype} on {device} expected")
+    n, m, d = t.shape
+    if (rows is not None and n != rows) or (heads is not None and m != heads) or (dim is not None and d != dim):
+        raise Q4Error(Q4_ESHAPE, f"{name}: shape {tuple(t.shape)}, ({rows}, {heads}, {dim}) expected")
+    rs, hs, es = t.stride()
+    if (es != 1 and d != 1) or (hs != d and m != 1):
+        raise Q4Error(Q4_ESHAPE, f"{name}: the heads of a row must lie one after the other")
+    return rs if n > 1 else m * d          # torch gives a single row any stride
+
+
+def _ints(t, name: str, device, n: int):
+    import torch
+    if t.dtype != torch.int32 or t.device != device:
+        raise Q4Error(Q4_EINVAL, f"{name}: {t.dtype} on {t.device}, int32 on {device} expected")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise Q4Error(Q4_ESHAPE, f"{name}: {n} contiguous entries expected")
+    return t.data_ptr()
+
+
+class PagedKV:
+    """A paged cache of keys and values: k and v [pages][page_size][heads][head_dim] (any strides,
+    the same for both, head_dim contiguous; a permuted view of pools laid out [pages][heads][..]
+    will do) and the page table, int32 [sequences][pages of a sequence].  Keeps the tensors alive."""
+
+    def __init__(self, k, v, table):
+        import torch
+        dt = _dtype_code(k)
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
+            raise Q4Error(Q4_ESHAPE, "k and v: one shape, type and layout [pages][page_size][heads][head_dim]")
+        if k.stride(3) != 1 and k.shape[3] != 1:
+            raise Q4Error(Q4_ESHAPE, "k and v: head_dim must be contiguous")
+        if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise Q4Error(Q4_ESHAPE, "table: int32 [sequences][pages of a sequence] expected")
+        if not (k.device == v.device == table.device) or k.device.type != "cuda":
+            raise Q4Error(Q4_EINVAL, "k, v and table: one CUDA device expected")
+        self.k, self.v, self.table = k, v, table
+        self.device, self.dtype = k.device, k.dtype
+        pages, size, heads, dim = k.shape
+        ps, ts, hs, _ = k.stride()
+        cols = table.shape[1]
+        self.args = q4gemv_kv(k.data_ptr(), v.data_ptr(), table.data_ptr(), pages, size, heads, dim, ps, ts, hs,
+                              table.stride(0) if table.shape[0] > 1 else cols, cols, dt)
+        self.ref = ctypes.byref(self.args)
 
 
 class Q4Gemv:
@@ -380,6 +497,133 @@ class Q4Gemv:
         self._check(q4gemv_run_stack_sharded(self.h, arr, len(layers_local), hidden, qkv_n, ffn,
                                              _ptr(x_in), _ptr(x_out), _stream(stream)))
         return x_out
+
+    # ---- token mixing: start int32 [sequences + 1] (rows of each sequence), length int32
+    # [sequences] (its tokens in the cache, the new ones counted), all on the handle's device ----
+
+    def _on_device(self, device):
+        if device.type != "cuda" or device.index != self.device:
+            raise Q4Error(Q4_EINVAL, f"tensors on {device}, the handle is on cuda:{self.device}")
+
+    def _stream_of(self, stream) -> int:
+        import torch
+        if stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def _new(self, shape, dtype, stream):
+        """An output, from the pool of the stream that writes it."""
+        import torch
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
+
+    def rope_freqs(self, rot: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0,
+                   trained: float = 0.0, lo: float = 1.0, hi: float = 32.0):
+        """float64 [rot/2] on the handle's device: radians per position of each pair."""
+        import torch
+        st, f = q4gemv_rope_freqs(kind, rot, base, factor, trained, lo, hi)
+        if st != Q4_OK:
+            raise Q4Error(st, f"rope_freqs: {q4gemv_strerror(st)}")
+        return torch.tensor(f, dtype=torch.float64, device=f"cuda:{self.device}")
+
+    def kv_append(self, cache, start, length, k, v, q=None, q_out=None, freqs=None,
+                  interleaved: bool = False, amp: float = 1.0, pos=None, stream=None):
+        """Appends k, v [rows][heads][head_dim] to the cache, k rotated; returns q
+        [rows][q_heads][head_dim] rotated (None without q).  freqs: float64 [rot/2] or None (no
+        rotation); pos: int32 [rows] rotation positions, by default the places in the cache."""
+        import torch
+        self._on_device(cache.device)
+        c = cache.args
+        n_seqs = length.shape[0]
+        if cache.table.shape[0] < n_seqs:
+            raise Q4Error(Q4_ESHAPE, "fewer page-table rows than sequences")
+        rows = k.shape[0]
+        ks = _heads(k, "k", cache.dtype, cache.device, None, c.n_heads, c.head_dim)
+        vs = _heads(v, "v", cache.dtype, cache.device, rows, c.n_heads, c.head_dim)
+        qs = qos = hq = 0
+        qp = qop = None
+        if q is not None:
+            hq = q.shape[1]
+            qs = _heads(q, "q", cache.dtype, cache.device, rows, None, c.head_dim)
+            if q_out is None:
+                q_out = self._new(q.shape, q.dtype, stream)
+            qos = _heads(q_out, "q_out", cache.dtype, cache.device, rows, hq, c.head_dim)
+            qp, qop = q.data_ptr(), q_out.data_ptr()
+        rope = None
+        if freqs is not None:
+            if freqs.dtype != torch.float64 or freqs.device != cache.device or not freqs.is_contiguous():
+                raise Q4Error(Q4_EINVAL, "freqs: contiguous float64 on the cache's device expected")
+            rope = q4gemv_rope(freqs.data_ptr(), 2 * freqs.numel(), int(interleaved), amp)
+        self._check(_lib.q4gemv_kv_append(
+            self.h, cache.ref, rows, n_seqs, _ints(start, "start", cache.device, n_seqs + 1),
+            _ints(length, "length", cache.device, n_seqs),
+            None if pos is None else _ints(pos, "pos", cache.device, rows), rope, qp, qs, hq,
+            k.data_ptr(), ks, v.data_ptr(), vs, qop, qos, self._stream_of(stream)))
+        return q_out if q is not None else None
+
+    def attn_paged(self, cache, start, length, q, out=None, scale: float | None = None,
+                   causal: bool = True, window: int = 0, max_new: int | None = None, stream=None):
+        """Attention of q [rows][q_heads][head_dim] over the cache (default scale
+        1/sqrt(head_dim)); max_new: the most new tokens of a sequence, where known."""
+        self._on_device(cache.device)
+        c = cache.args
+        n_seqs = length.shape[0]
+        if cache.table.shape[0] < n_seqs:
+            raise Q4Error(Q4_ESHAPE, "fewer page-table rows than sequences")
+        qs = _heads(q, "q", cache.dtype, cache.device, None, None, c.head_dim)
+        rows, hq = q.shape[0], q.shape[1]
+        if out is None:
+            out = self._new(q.shape, q.dtype, stream)
+        os_ = _heads(out, "out", cache.dtype, cache.device, rows, hq, c.head_dim)
+        self._check(_lib.q4gemv_attn_paged(
+            self.h, cache.ref, rows, n_seqs, _ints(start, "start", cache.device, n_seqs + 1),
+            _ints(length, "length", cache.device, n_seqs), max(1, rows) if max_new is None else max_new,
+            q.data_ptr(), qs, hq, out.data_ptr(), os_,
+            c.head_dim ** -0.5 if scale is None else scale, int(causal), window, self._stream_of(stream)))
+        return out
+
+    def linattn(self, q, k, v, log_decay, start, state, state_out=None, slots=None, scale: float = 1.0,
+                out=None, max_new: int | None = None, stream=None):
+        """Linear attention with decay: q, k [rows][qk_heads][k_dim], v [rows][v_heads][v_dim],
+        log_decay float32 [rows][v_heads] (an expanded row: fixed decays), state float32
+        [slots][v_heads][k_dim][v_dim] (updated in place unless state_out is given; None: from
+        zeros into state_out).  Returns (out, state_out)."""
+        import torch
+        if state_out is None:
+            state_out = state
+        if state_out is None:
+            raise Q4Error(Q4_EINVAL, "linattn: neither state nor state_out")
+        dev = state_out.device
+        self._on_device(dev)
+        n_seqs = start.shape[0] - 1
+        dt = _dtype_code(q)
+        qs = _heads(q, "q", q.dtype, dev)
+        rows, hk, dk = q.shape
+        ks = _heads(k, "k", q.dtype, dev, rows, hk, dk)
+        hv, dv = v.shape[1], v.shape[2]
+        vs = _heads(v, "v", q.dtype, dev, rows)
+        if out is None:
+            out = self._new((rows, hv, dv), q.dtype, stream)
+        os_ = _heads(out, "out", q.dtype, dev, rows, hv, dv)
+        if log_decay.dtype != torch.float32 or log_decay.device != dev or log_decay.shape != (rows, hv) or \
+                (hv > 1 and log_decay.stride(1) != 1):
+            raise Q4Error(Q4_ESHAPE, f"log_decay: float32 [{rows}][{hv}] on {dev} expected")
+        n_slots = state_out.shape[0]
+        for t in (state, state_out):
+            if t is not None and (t.dtype != torch.float32 or t.device != dev or not t.is_contiguous() or
+                                  t.shape != (n_slots, hv, dk, dv)):
+                raise Q4Error(Q4_ESHAPE, f"state: contiguous float32 [{n_slots}][{hv}][{dk}][{dv}] on {dev} expected")
+        a = q4gemv_linattn_args(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state), state_out.data_ptr(),
+            None if slots is None else _ints(slots, "slots", dev, n_seqs), out.data_ptr(), qs, ks, vs,
+            log_decay.stride(0) if rows > 1 else hv, os_, n_slots, hk, hv, dk, dv, scale, dt)
+        self._check(_lib.q4gemv_linattn(self.h, a, rows, n_seqs, _ints(start, "start", dev, n_seqs + 1),
+                                        max(1, rows) if max_new is None else max_new, self._stream_of(stream)))
+        return out, state_out
 
     def sync_status(self, stream=None) -> int:
         return q4gemv_sync_status(self.h, _stream(stream))

@@ -10,9 +10,10 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libq4gemv.so")
-SOURCES = ["q4gemv_api.cu", "q4gemv_noalloc.cu"]
+SOURCES = ["q4gemv_api.cu", "q4gemv_noalloc.cu", "mix_api.cu"]
 HEADERS = ["device_common.cuh", "partition.cuh", "gemv_dp2a.cuh", "gemv_mma.cuh", "stack.cuh",
-           "gemm_tc.cuh", "gemv_swiglu.cuh", "gemv_tcs.cuh"]
+           "gemm_tc.cuh", "gemv_swiglu.cuh", "gemv_tcs.cuh", "ctx_view.h", "mix_common.cuh",
+           "kv_append.cuh", "attn_rows.cuh", "linattn.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

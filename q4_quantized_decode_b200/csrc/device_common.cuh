@@ -221,7 +221,7 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 
 // Device error codes written to the handle's error word.
-enum : int { kDevOk = 0, kDevTimeout = 1, kDevConcurrent = 2 };
+enum : int { kDevOk = 0, kDevTimeout = 1, kDevConcurrent = 2, kDevIndex = 3 };
 
 __device__ __forceinline__ void set_device_error(int* err, int code) {
     if (err) atomicCAS(err, 0, code);

@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "../../include/q4gemv.h"
+#include "ctx_view.h"
 #include "gemv_dp2a.cuh"
 #include "gemm_tc.cuh"
 #include "gemv_mma.cuh"
@@ -717,6 +718,7 @@ const char* q4gemv_strerror(int status) {
         case Q4_ETIMEOUT: return "bounded device wait timed out";
         case Q4_EFAULTINJ: return "injected fault";
         case Q4_ECONCURRENT: return "overlapping calls on one handle";
+        case Q4_EINDEX: return "page, place or state slot out of range";
         default: return "unknown status";
     }
 }
@@ -1644,9 +1646,21 @@ int q4gemv_sync_status(q4gemv_t h, q4gemv_stream_t stream) {
         Q4_CUDA(h, cudaMemset(h->err, 0, sizeof(int)));
         if (word == q4::kDevTimeout) return fail(h, Q4_ETIMEOUT, "device wait timed out");
         if (word == q4::kDevConcurrent) return fail(h, Q4_ECONCURRENT, "overlapping calls detected");
+        if (word == q4::kDevIndex) return fail(h, Q4_EINDEX, "a page, place or state slot was out of range");
         return fail(h, Q4_ECUDA, "device error word %d", word);
     }
     return Q4_OK;
 }
 
 }  // extern "C"
+
+q4::CtxView q4::ctx_view(q4gemv_t h) {
+    CtxView v;
+    v.device = h->device;
+    v.sms = h->sms;
+    v.fail_launch = h->fault == kFaultLaunch;
+    v.err = h->err;
+    return v;
+}
+
+int q4::ctx_fail(q4gemv_t h, int status, const char* text) { return fail(h, status, "%s", text); }

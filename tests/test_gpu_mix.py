@@ -1,0 +1,761 @@
+"""Token mixing (q4gemv_kv_append, q4gemv_attn_paged, q4gemv_linattn) through
+the binding against plain 64-bit forms.
+
+Tolerances, from the arithmetic (u = half a step of the 16-bit type):
+  append  an output is rounded once (u of it) from 32-bit products whose
+          cosines and sines are off by a few 2^-24 (argument and function), so
+          u |y| + 2^-20 (|a| + |b|) amp.
+  attend  scores are 32-bit sums of head_dim products (at most head_dim 2^-23
+          of their magnitudes, a factor on the weights), weights may be rounded
+          once to the type before they meet v (u each; for f16 also 2^-25 of the
+          largest weight each, its subnormals), sums of up to len terms in 32
+          bits, and one final rounding:
+          (u + 2 head_dim 2^-23 mags + 2^-18) A + len 2^-25 max|v| + u |o|, with A the
+          weighted magnitudes of v (2^-18: exp2 and the sums of up to 2^11
+          steps of 2^-23 in tiles).
+  linear  state: 32-bit sums of a token's terms, at most (tokens + 64) 2^-22 of
+          their magnitudes; out: operands of the products may be rounded to
+          11 bits once each (2 * 2^-11), plus the same, plus u |o|.
+"""
+import pytest
+
+from tests import mix_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import q4_quantized_decode_b200 as q4  # noqa: E402
+
+DTYPES = [torch.float16, torch.bfloat16]
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def eng():
+    e = q4.Q4Gemv(0)
+    yield e
+    e.close()
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def starts(new):
+    s = [0]
+    for n in new:
+        s.append(s[-1] + n)
+    return s
+
+
+def gpu_pool(x):
+    """The pool on the GPU with the same strides (a permuted view stays one)."""
+    if x.is_contiguous():
+        return x.to(DEV)
+    return x.transpose(1, 2).to(DEV).transpose(1, 2)
+
+
+def close(got, want, tol, what):
+    got = got.detach().to("cpu", torch.float64)
+    assert torch.isfinite(got).all(), f"{what}: not finite"
+    over = (got - want).abs() - tol
+    worst = over.max().item() if over.numel() else -1.0
+    assert worst <= 0, f"{what}: {worst:.3e} over the tolerance at {int(over.argmax())}"
+
+
+# ---- append -----------------------------------------------------------------
+
+class AppendCase:
+    def __init__(self, new, ctx, hq, hkv, dim, page, dtype, seed=0, head_major=False, fused=True):
+        gen = torch.Generator().manual_seed(seed)
+        self.new, self.dtype, self.dim, self.hq, self.hkv = new, dtype, dim, hq, hkv
+        self.length = [n + c for n, c in zip(new, ctx)]
+        self.rows = sum(new)
+        self.table, pool = ref.table_of(self.length, page, gen)
+        self.k0 = ref.paged(pool, page, hkv, dim, dtype, gen, head_major)
+        self.v0 = ref.paged(pool, page, hkv, dim, dtype, gen, head_major)
+        w = (hq + 2 * hkv) * dim
+        qkv = torch.randn(self.rows, w, generator=gen).to(dtype)
+        cut = lambda x, a, h: x[:, a * dim:(a + h) * dim].unflatten(1, (h, dim))  # noqa: E731
+        self.q, self.k, self.v = cut(qkv, 0, hq), cut(qkv, hq, hkv), cut(qkv, hq + hkv, hkv)
+        g = qkv.to(DEV)
+        self.gq, self.gk, self.gv = cut(g, 0, hq), cut(g, hq, hkv), cut(g, hq + hkv, hkv)
+        if not fused:
+            self.gq, self.gk, self.gv = (x.contiguous() for x in (self.gq, self.gk, self.gv))
+        self.cache = q4.PagedKV(gpu_pool(self.k0), gpu_pool(self.v0), self.table.to(DEV))
+        self.start, self.glen = ints(starts(new)), ints(self.length)
+        self.pos = torch.tensor([p for n, l in zip(new, self.length) for p in range(l - n, l)], dtype=torch.int64)
+        self.seq = [s for s, n in enumerate(new) for _ in range(n)]
+        self.page = page
+
+    def check(self, qo, freqs, interleaved=False, amp=1.0, pos=None):
+        pos = self.pos if pos is None else pos
+        u, t = ref.half_step(self.dtype), ref.tiny(self.dtype)
+        for name, x, got in (("q", self.q, qo), ("k", self.k, None)):
+            want, mag = ref.rotate(x, pos, freqs, interleaved, amp)
+            if got is None:
+                at = self.pos
+                pg = self.table[self.seq, at // self.page].long()
+                kd = self.cache.k.cpu()
+                close(kd[pg, at % self.page], want, u * want.abs() + 2.0 ** -20 * mag + t, "k")
+                rest = torch.ones(kd.shape[:2], dtype=torch.bool)
+                rest[pg, at % self.page] = False
+                assert torch.equal(kd[rest], self.k0[rest]), "slots of no new token changed"
+                vd = self.cache.v.cpu()
+                assert torch.equal(vd[pg, at % self.page], self.v)
+                assert torch.equal(vd[rest], self.v0[rest])
+            elif got is not False:
+                close(got, want, u * want.abs() + 2.0 ** -20 * mag + t, name)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,rot", [(128, 128), (128, 64), (64, 64), (96, 96), (80, 32), (256, 64), (8, 8), (64, 20),
+                                     (128, 0), (72, 2), (64, 34)])
+def test_append_layouts(eng, dtype, interleaved, dim, rot):
+    c = AppendCase([3, 1, 0, 17], [0, 31, 5, 100], 6, 2, dim, 16, dtype, seed=dim + rot)
+    st, f = q4.q4gemv_rope_freqs(q4.ROPE_PLAIN, rot, 10000.0)
+    freqs = torch.tensor(f, dtype=torch.float64, device=DEV) if rot else None
+    qo = eng.kv_append(c.cache, c.start, c.glen, c.gk, c.gv, q=c.gq, freqs=freqs, interleaved=interleaved, amp=1.25)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(qo, f, interleaved, 1.25 if rot else 1.0)
+
+
+@pytest.mark.parametrize("page,head_major", [(1, False), (7, True), (24, False), (64, True), (1000, False)])
+def test_append_pages_and_layouts(eng, page, head_major):
+    c = AppendCase([5, 40, 1], [99, 0, 1000], 8, 8, 64, page, torch.float16, seed=page, head_major=head_major, fused=False)
+    f = eng.rope_freqs(64)
+    qo = eng.kv_append(c.cache, c.start, c.glen, c.gk, c.gv, q=c.gq, freqs=f)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(qo, f.cpu())
+
+
+@pytest.mark.parametrize("kind,factor", [(q4.ROPE_PLAIN, 1.0), (q4.ROPE_LINEAR, 4.0), (q4.ROPE_BY_PARTS, 16.0)])
+def test_append_far_positions(eng, kind, factor):
+    """Positions of a million: the angle has to be taken in 64 bits."""
+    c = AppendCase([2, 9], [0, 50], 4, 1, 128, 32, torch.float16, seed=3)
+    f = eng.rope_freqs(128, base=1e6, kind=kind, factor=factor, trained=32768.0)
+    pos = torch.tensor([0, 1] + [999_983 + 7 * i for i in range(8)] + [2**31 - 1], dtype=torch.int64)
+    qo = eng.kv_append(c.cache, c.start, c.glen, c.gk, c.gv, q=c.gq, freqs=f, pos=ints(pos.tolist()))
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(qo, f.cpu(), pos=pos)
+
+
+def test_append_in_place_and_without_queries(eng):
+    c = AppendCase([6], [20], 5, 1, 64, 16, torch.bfloat16, seed=4, fused=False)
+    f = eng.rope_freqs(48)
+    q = c.gq.clone()
+    assert eng.kv_append(c.cache, c.start, c.glen, c.gk, c.gv, q=q, q_out=q, freqs=f, interleaved=True) is q
+    c.check(q, f.cpu(), True)
+    c = AppendCase([6], [20], 5, 1, 64, 16, torch.bfloat16, seed=5)
+    assert eng.kv_append(c.cache, c.start, c.glen, c.gk, c.gv, freqs=f) is None
+    c.check(False, f.cpu())
+    assert eng.sync_status() == q4.Q4_OK
+
+
+def test_append_leaves_other_rows(eng):
+    """Rows behind the last sequence are neither read nor written."""
+    c = AppendCase([4, 2], [3, 0], 2, 1, 64, 8, torch.float16, seed=6, fused=False)
+    start = ints([0, 4, 5])                              # the last row is nobody's
+    length = ints([7, 1])
+    out = torch.full_like(c.gq, 7.0)
+    eng.kv_append(c.cache, start, length, c.gk, c.gv, q=c.gq, q_out=out, freqs=eng.rope_freqs(64))
+    assert eng.sync_status() == q4.Q4_OK
+    assert (out[5] == 7.0).all() and not (out[:5] == 7.0).all()
+
+
+def test_append_infinite_values_pass_where_not_rotated(eng):
+    c = AppendCase([1], [0], 1, 1, 64, 8, torch.float16, seed=7, fused=False)
+    for il in (False, True):
+        q = c.gq.clone()
+        q[0, 0, 20] = float("nan")
+        q[0, 0, 23] = float("inf")
+        out = eng.kv_append(c.cache, c.start, c.glen, c.gk, c.gv, q=q, freqs=eng.rope_freqs(20), interleaved=il)
+        assert torch.isnan(out[0, 0, 20]) and torch.isinf(out[0, 0, 23])
+        assert torch.isfinite(out[0, 0, :20]).all() and torch.equal(out[0, 0, 24:], q[0, 0, 24:])
+
+
+def test_append_bad_pages_are_reported(eng):
+    c = AppendCase([2, 3], [0, 14], 2, 1, 64, 8, torch.float16, seed=8)
+    k0 = c.cache.k.clone()
+    c.cache.table[0, 0] = c.k0.shape[0]                  # past the pool
+    c.cache.table[1, 2] = -5
+    qo = eng.kv_append(c.cache, c.start, c.glen, c.gk, c.gv, q=c.gq, freqs=eng.rope_freqs(64))
+    assert eng.sync_status() == q4.Q4_EINDEX
+    assert eng.sync_status() == q4.Q4_OK
+    want, mag = ref.rotate(c.q, c.pos, eng.rope_freqs(64).cpu())
+    close(qo, want, 2.0 ** -11 * want.abs() + 2.0 ** -20 * mag + 2.0 ** -25, "q")
+    changed = (c.cache.k != k0).any(-1).any(-1)          # rows 14, 15 of sequence 1 only (place 16 is in the bad page)
+    assert int(changed.sum()) == 2
+    # a length under the new tokens' count: negative places
+    eng.kv_append(c.cache, c.start, ints([1, 17]), c.gk, c.gv)
+    assert eng.sync_status() == q4.Q4_EINDEX
+    # past the table's columns
+    eng.kv_append(c.cache, c.start, ints([2, 8 * c.table.shape[1] + 3]), c.gk, c.gv)
+    assert eng.sync_status() == q4.Q4_EINDEX
+
+
+# ---- attend -----------------------------------------------------------------
+
+class AttendCase:
+    def __init__(self, new, length, hq, hkv, dim, page, dtype, seed=0, head_major=False, poison=True, amp=1.0):
+        gen = torch.Generator().manual_seed(seed)
+        self.new, self.length, self.hq, self.hkv, self.dim, self.dtype = new, length, hq, hkv, dim, dtype
+        self.rows = sum(new)
+        self.table, pool = ref.table_of(length, page, gen)
+        self.k, self.v = (ref.paged(pool, page, hkv, dim, dtype, gen, head_major) for _ in range(2))
+        if poison:                                       # what no token has written is NaN
+            used = torch.zeros(pool, page, dtype=torch.bool)
+            for s, l in enumerate(length):
+                j = torch.arange(l)
+                used[self.table[s, j // page].long(), j % page] = True
+            self.k[~used] = float("nan")
+            self.v[~used] = float("nan")
+        self.q = (amp * torch.randn(self.rows, hq, dim, generator=gen)).to(dtype)
+        self.cache = q4.PagedKV(gpu_pool(self.k), gpu_pool(self.v), self.table.to(DEV))
+        self.gq, self.start, self.glen = self.q.to(DEV), ints(starts(new)), ints(length)
+
+    def run(self, eng, **kw):
+        return eng.attn_paged(self.cache, self.start, self.glen, self.gq, **kw)
+
+    def check(self, out, scale=None, causal=True, window=0, seqs=None, heads=None):
+        scale = self.dim ** -0.5 if scale is None else scale
+        u = ref.half_step(self.dtype)
+        out = out.cpu()
+        at = starts(self.new)
+        for s, (n, l) in enumerate(zip(self.new, self.length)):
+            if n == 0 or (seqs is not None and s not in seqs):
+                continue
+            for h in range(self.hq) if heads is None else heads:
+                kv = h // (self.hq // self.hkv)
+                k, v = (ref.gather(x, self.table, s, l, kv) for x in (self.k, self.v))
+                o, a, mags = ref.attend(self.q[at[s]:at[s + 1], h], k, v, l - n, scale, causal, window)
+                top = torch.nan_to_num(v.double(), 0.0, 0.0, 0.0).abs().amax() if l else 0.0
+                tol = (u + 2 * self.dim * 2.0 ** -23 * mags[:, None] + 2.0 ** -18) * a + \
+                    l * 2.0 ** -25 * top + u * o.abs() + ref.tiny(self.dtype)
+                close(out[at[s]:at[s + 1], h], o, tol, f"sequence {s}, head {h}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hq,hkv,dim", [(5, 1, 128), (8, 8, 64), (8, 2, 64), (6, 2, 128), (4, 1, 256), (3, 3, 96),
+                                        (2, 1, 8), (20, 1, 80), (40, 2, 64), (4, 2, 248)])
+def test_attend_single_tokens(eng, dtype, hq, hkv, dim):
+    c = AttendCase([1] * 6, [1, 2, 31, 64, 257, 700], hq, hkv, dim, 16, dtype, seed=hq + dim)
+    out = c.run(eng, max_new=1)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("page,head_major", [(1, False), (5, False), (16, True), (24, False), (100, True), (1024, False)])
+def test_attend_pages(eng, dtype, page, head_major):
+    c = AttendCase([1, 3, 70], [300, 77, 211], 4, 2, 64, page, dtype, seed=page, head_major=head_major)
+    out = c.run(eng, max_new=70)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new,length", [([169], [169]), ([128, 0, 1, 33], [128, 40, 513, 1000]), ([200], [1300]),
+                                        ([257, 64], [257, 65]), ([600], [600])])
+@pytest.mark.parametrize("hq,hkv,dim", [(5, 1, 128), (4, 4, 64), (2, 1, 256), (3, 1, 72)])
+def test_attend_chunks(eng, dtype, new, length, hq, hkv, dim):
+    c = AttendCase(new, length, hq, hkv, dim, 16, dtype, seed=sum(new) + dim)
+    out = c.run(eng, max_new=max(new))
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(out)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 1), (True, 7), (True, 130), (True, 100000), (False, 0), (False, 40)])
+@pytest.mark.parametrize("new,length", [([1, 1], [500, 3]), ([4, 5], [260, 9]), ([150], [400])])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_masks(eng, causal, window, new, length, dim):
+    c = AttendCase(new, length, 4, 2, dim, 24, torch.float16, seed=window + sum(new))
+    out = c.run(eng, causal=causal, window=window, max_new=max(new))
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(out, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("max_new", [1, 5, 1000])
+def test_attend_max_new_is_only_a_hint(eng, max_new):
+    c = AttendCase([1, 150, 0, 9], [900, 170, 8, 300], 6, 2, 128, 16, torch.float16, seed=9)
+    out = c.run(eng, max_new=max_new)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(out)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [3, 200])
+def test_attend_rows_that_see_nothing(eng, dim, new):
+    """A length under the count of the new tokens: the first rows stand before
+    the cache's beginning and see nothing; length 0: no row sees anything."""
+    c = AttendCase([new, new], [new - 2, 0], 2, 1, dim, 16, torch.float16, seed=dim)
+    out = c.run(eng, max_new=new)
+    assert eng.sync_status() == q4.Q4_OK
+    assert (out[:2] == 0).all() and (out[new:] == 0).all()
+    c.check(out)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [4, 180])
+def test_attend_non_finite_values_of_unseen_tokens(eng, bad, dim, new):
+    """A later token of the chunk, or one before the window, holds NaN or Inf in
+    its key and value: rows that do not see it are unaffected; rows that see it
+    are not finite."""
+    c = AttendCase([new], [new + 50], 2, 1, dim, 16, torch.float16, seed=dim + new)
+    j = new + 50 - 2                                     # the last but one token
+    pg, at = int(c.table[0, j // 16]), j % 16
+    for pool in (c.k, c.v, c.cache.k, c.cache.v):
+        pool[pg, at, 0, 3] = bad
+    out = c.run(eng, max_new=new)
+    assert eng.sync_status() == q4.Q4_OK
+    assert torch.isfinite(out[:new - 2]).all()
+    if bad != bad:
+        assert torch.isnan(out[new - 2:]).all()
+    clean = AttendCase([new], [new + 50], 2, 1, dim, 16, torch.float16, seed=dim + new)
+    same = clean.run(eng, max_new=new)
+    clean.check(same)
+    same[:new - 2] = out[:new - 2]
+    clean.check(same)
+    # before the window
+    w = 40
+    c2 = AttendCase([new], [new + 50], 2, 1, dim, 16, torch.float16, seed=dim + new)
+    pg, at = int(c2.table[0, 0]), 2
+    for pool in (c2.k, c2.v, c2.cache.k, c2.cache.v):
+        pool[pg, at, 0, :] = bad
+    out = c2.run(eng, max_new=new, window=w)
+    assert eng.sync_status() == q4.Q4_OK
+    c2.check(out, window=w)
+
+
+def test_attend_large_scores(eng):
+    """Scores of hundreds: one token takes all the weight; the running maximum
+    has to follow."""
+    for dim, new in ((64, 1), (128, 2), (128, 140), (64, 140), (256, 3)):
+        c = AttendCase([new], [600], 4, 2, dim, 16, torch.float16, seed=dim, amp=30.0)
+        out = c.run(eng, max_new=new)
+        c.check(out)
+        out = c.run(eng, max_new=new, scale=0.0)
+        c.check(out, scale=0.0)
+        out = c.run(eng, max_new=new, scale=-0.02)
+        c.check(out, scale=-0.02)
+    assert eng.sync_status() == q4.Q4_OK
+
+
+def test_attend_strides_and_rows_of_no_sequence(eng):
+    for new in ([1, 2], [90, 40]):
+        c = AttendCase(new, [70 + new[0], 200], 4, 2, 64, 16, torch.bfloat16, seed=11)
+        rows = c.rows
+        wide = torch.full((rows + 3, 4 * 64 + 24), 5.0, dtype=c.dtype, device=DEV)
+        q = wide.clone()[:, :256].unflatten(1, (4, 64))
+        q[:rows] = c.gq
+        out = wide[:, 8:264].unflatten(1, (4, 64))
+        got = eng.attn_paged(c.cache, c.start, c.glen, q, out=out, max_new=max(new))
+        assert got is out and eng.sync_status() == q4.Q4_OK
+        c.check(out[:rows])
+        assert (out[rows:] == 5.0).all() and (wide[:, :8] == 5.0).all() and (wide[:, 264:] == 5.0).all()
+
+
+def test_attend_shared_pages(eng):
+    """Two sequences with the same prefix pages."""
+    c = AttendCase([1, 2], [64, 64], 4, 2, 64, 16, torch.float16, seed=12, poison=False)
+    c.table[1, :3] = c.table[0, :3]
+    c.cache.table.copy_(c.table)
+    c.check(c.run(eng, max_new=2))
+    assert eng.sync_status() == q4.Q4_OK
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_attend_bad_pages_are_left_out(eng, new):
+    c = AttendCase([new, new], [200, 300], 4, 2, 128, 16, torch.float16, seed=13)
+    good = c.cache.table.clone()
+    c.cache.table[0, 3] = 10 ** 6
+    c.cache.table[0, 4] = -1
+    out = c.run(eng, max_new=new)
+    assert eng.sync_status() == q4.Q4_EINDEX
+    assert torch.isfinite(out).all()
+    c.check(out, seqs=[1])
+    # the first sequence as if those 32 tokens were not there
+    u = 2.0 ** -11
+    for h in range(4):
+        k, v = (ref.gather(x, c.table, 0, 200, h // 2) for x in (c.k, c.v))
+        keep = torch.cat((torch.arange(48), torch.arange(80, 200)))
+        o, a, mags = ref.attend(c.q[:new, h], k[keep], v[keep], 200 - new - 32, 128 ** -0.5)
+        tol = (u + 256 * 2.0 ** -23 * mags[:, None] + 2.0 ** -18) * a + 200 * 2.0 ** -25 * 6 + u * o.abs() + 2.0 ** -25
+        close(out[:new, h], o, tol, "without the bad pages")
+    c.cache.table.copy_(good)
+    c.check(c.run(eng, max_new=new))
+    # a length past the table's columns
+    eng.attn_paged(c.cache, c.start, ints([200, 16 * c.table.shape[1] + 40]), c.gq, max_new=new)
+    assert eng.sync_status() == q4.Q4_EINDEX
+
+
+def test_attend_is_deterministic_and_follows_a_graph(eng):
+    """A captured call replayed after the lengths, tables and queries changed."""
+    for new in (1, 120):
+        c = AttendCase([new, new, new], [900, 130, 350], 8, 2, 128, 16, torch.float16, seed=14)
+        a, b = c.run(eng, max_new=new), c.run(eng, max_new=new)
+        assert torch.equal(a, b)
+        out = torch.zeros_like(c.gq)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            eng.attn_paged(c.cache, c.start, c.glen, c.gq, out=out, max_new=new)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, a)
+        d = AttendCase([new, new, new], [500, 700, 121], 8, 2, 128, 16, torch.float16, seed=15)
+        n, cols = d.cache.k.shape[0], d.table.shape[1]
+        assert n <= c.cache.k.shape[0] and cols <= c.table.shape[1]
+        c.glen.copy_(d.glen)
+        c.gq.copy_(d.gq)
+        c.cache.table.fill_(-1)
+        c.cache.table[:, :cols].copy_(d.cache.table)
+        c.cache.k[:n].copy_(d.cache.k)
+        c.cache.v[:n].copy_(d.cache.v)
+        g.replay()
+        torch.cuda.synchronize()
+        d.check(out)
+        assert eng.sync_status() == q4.Q4_OK
+
+
+def test_attend_long_context_offsets(eng):
+    """A pool of more than 2^31 elements: the far pages' offsets pass 32 bits."""
+    page, hkv, dim = 64, 8, 128
+    pool = 2 ** 31 // (page * hkv * dim) + 40
+    k = torch.zeros(pool, page, hkv, dim, dtype=torch.float16, device=DEV)
+    v = torch.zeros_like(k)
+    gen = torch.Generator().manual_seed(1)
+    for new in (1, 80):
+        table = torch.arange(pool - 7, pool, dtype=torch.int32)[None].flip(1).contiguous()
+        kk, vv = (torch.randn(7 * page, hkv, dim, generator=gen).half() for _ in range(2))
+        k[pool - 7:] = kk.view(7, page, hkv, dim).to(DEV)
+        v[pool - 7:] = vv.view(7, page, hkv, dim).to(DEV)
+        q = torch.randn(new, 2 * hkv, dim, generator=gen).half()
+        cache = q4.PagedKV(k, v, table.to(DEV))
+        out = eng.attn_paged(cache, ints([0, new]), ints([400]), q.to(DEV), max_new=new).cpu()
+        assert eng.sync_status() == q4.Q4_OK
+        kc, vc = (x.view(7, page, hkv, dim).flip(0).reshape(-1, hkv, dim)[:400] for x in (kk, vv))
+        for h in (0, 15):
+            o, a, mags = ref.attend(q[:, h], kc[:, h // 2], vc[:, h // 2], 400 - new, dim ** -0.5)
+            tol = (2.0 ** -11 + 256 * 2.0 ** -23 * mags[:, None] + 2.0 ** -18) * a + 400 * 2.0 ** -25 * 6 + \
+                2.0 ** -11 * o.abs() + 2.0 ** -25
+            close(out[:, h], o, tol, f"head {h}")
+
+
+# ---- linear -----------------------------------------------------------------
+
+class LinearCase:
+    def __init__(self, new, hk, hv, dk, dv, dtype, seed=0, fixed=False, slots=None, rate=(-1.0, -8.0)):
+        gen = torch.Generator().manual_seed(seed)
+        self.new, self.hk, self.hv, self.dk, self.dv, self.dtype = new, hk, hv, dk, dv, dtype
+        rows = self.rows = sum(new)
+        n = len(new)
+        self.slots = torch.randperm(n + 1, generator=gen)[:n].to(torch.int32) if slots is None else slots
+        qkv = torch.randn(rows, 2 * hk * dk + hv * dv, generator=gen)
+        qkv[:, :2 * hk * dk] *= dk ** -0.5
+        qkv = qkv.to(dtype)
+        cut = lambda x: (x[:, :hk * dk].unflatten(1, (hk, dk)), x[:, hk * dk:2 * hk * dk].unflatten(1, (hk, dk)),  # noqa: E731
+                         x[:, 2 * hk * dk:].unflatten(1, (hv, dv)))
+        self.q, self.k, self.v = cut(qkv)
+        self.gq, self.gk, self.gv = cut(qkv.to(DEV))
+        r = 2.0 ** (rate[0] + (rate[1] - rate[0]) * torch.rand(1 if fixed else rows, hv, generator=gen))
+        self.g = (-r).expand(rows, hv) if fixed else -r
+        self.gg = (-r).to(DEV).expand(rows, hv) if fixed else (-r).to(DEV)
+        self.state = torch.randn(n + 1, hv, dk, dv, generator=gen)
+        self.start = ints(starts(new))
+
+    def run(self, eng, state=None, **kw):
+        kw.setdefault("slots", self.slots.to(DEV))
+        kw.setdefault("max_new", max([1] + self.new))
+        return eng.linattn(self.gq, self.gk, self.gv, self.gg, self.start,
+                           self.state.to(DEV) if state is None else state, **kw)
+
+    def check(self, out, state, scale=1.0, zero=False, seqs=None, heads=None):
+        u = ref.half_step(self.dtype)
+        out, state = out.cpu(), state.cpu()
+        at = starts(self.new)
+        for s, n in enumerate(self.new):
+            if seqs is not None and s not in seqs:
+                continue
+            sl = slice(at[s], at[s + 1])
+            for h in range(self.hv) if heads is None else heads:
+                hk = h // (self.hv // self.hk)
+                s0 = self.state[self.slots[s], h]
+                o, S, ao, A = ref.linear(self.q[sl, hk], self.k[sl, hk], self.v[sl, h], self.g[sl, h],
+                                         torch.zeros_like(s0) if zero else s0, scale)
+                sums = (n + 64) * 2.0 ** -22
+                close(state[self.slots[s], h], S, sums * A, f"state {s}, head {h}")
+                close(out[sl, h], o, (2.0 ** -10 + sums) * ao + u * o.abs() + ref.tiny(self.dtype),
+                      f"sequence {s}, head {h}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hk,hv,dk,dv", [(1, 1, 128, 128), (2, 6, 64, 64), (1, 3, 128, 64), (2, 2, 64, 128),
+                                         (1, 1, 8, 8), (1, 2, 72, 40), (1, 1, 256, 256), (3, 3, 136, 24)])
+def test_linear_single_tokens(eng, dtype, hk, hv, dk, dv):
+    c = LinearCase([1, 1, 0, 2, 1], hk, hv, dk, dv, dtype, seed=dk + dv)
+    out, state = c.run(eng, scale=0.5)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(out, state, scale=0.5)
+    unused = (set(range(6)) - set(c.slots.tolist())).pop()
+    assert torch.equal(state[unused].cpu(), c.state[unused])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fixed", [False, True])
+@pytest.mark.parametrize("new", [[64], [65, 0, 1, 63], [130, 17], [300], [5, 128, 127]])
+@pytest.mark.parametrize("hk,hv,dk,dv", [(1, 2, 128, 128), (2, 2, 64, 64), (1, 1, 64, 128), (1, 1, 24, 40), (1, 1, 256, 72)])
+def test_linear_prompts(eng, dtype, fixed, new, hk, hv, dk, dv):
+    c = LinearCase(new, hk, hv, dk, dv, dtype, seed=sum(new) + dk, fixed=fixed)
+    out, state = c.run(eng)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(out, state)
+
+
+@pytest.mark.parametrize("rate", [(3.0, 7.0), (-14.0, -20.0)])
+def test_linear_strong_and_weak_decays(eng, rate):
+    """Decays of e^-8 to e^-128 a token (differences of running sums lose all
+    digits; a chunk's product underflows) and of nearly one."""
+    for new in ([1, 3], [200, 70]):
+        c = LinearCase(new, 1, 2, 64, 64, torch.float16, seed=21, rate=rate)
+        out, state = c.run(eng)
+        assert eng.sync_status() == q4.Q4_OK
+        c.check(out, state)
+
+
+def test_linear_decay_of_minus_infinity_clears(eng):
+    for new in ([3], [150]):
+        c = LinearCase(new, 1, 1, 64, 64, torch.float16, seed=22)
+        at = new[0] // 2
+        c.g = c.g.clone()
+        c.g[at] = -float("inf")
+        c.gg[at] = -float("inf")
+        out, state = c.run(eng)
+        assert eng.sync_status() == q4.Q4_OK
+        c.check(out, state)
+
+
+def test_linear_zero_state_and_out_of_place(eng):
+    for new in ([1, 2], [100, 30]):
+        c = LinearCase(new, 1, 2, 64, 128, torch.bfloat16, seed=23)
+        s0 = c.state.to(DEV)
+        so = torch.full_like(s0, 9.0)
+        out, state = c.run(eng, state=s0, state_out=so)
+        assert state is so and torch.equal(s0.cpu(), c.state)
+        c.check(out, state)
+        so2 = torch.full_like(s0, 9.0)
+        out, state = eng.linattn(c.gq, c.gk, c.gv, c.gg, c.start, None, state_out=so2, slots=c.slots.to(DEV),
+                                 max_new=max(new))
+        c.check(out, state, zero=True)
+        unused = (set(range(3)) - set(c.slots.tolist())).pop()
+        assert (so2[unused] == 9.0).all()
+    assert eng.sync_status() == q4.Q4_OK
+
+
+def test_linear_in_pieces_is_the_whole(eng):
+    """A prompt in chunks, then token by token, ends in the state of one pass."""
+    c = LinearCase([200], 1, 2, 128, 128, torch.float16, seed=24, slots=torch.tensor([0], dtype=torch.int32))
+    whole, end = c.run(eng)
+    c.check(whole, end)
+    state = c.state.to(DEV)
+    parts = []
+    for a, b in [(0, 90), (90, 91), (91, 190)] + [(i, i + 1) for i in range(190, 200)]:
+        o, _ = eng.linattn(c.gq[a:b], c.gk[a:b], c.gv[a:b], c.gg[a:b], ints([0, b - a]), state, max_new=b - a)
+        parts.append(o)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(torch.cat(parts), state)
+
+
+def test_linear_bad_slots_are_left_out(eng):
+    for new in ([1, 1, 1], [70, 80, 90]):
+        c = LinearCase(new, 1, 1, 64, 64, torch.float16, seed=25)
+        bad = c.slots.clone()
+        bad[1] = 99
+        out0 = torch.full((c.rows, 1, 64), 3.0, dtype=torch.float16, device=DEV)
+        out, state = c.run(eng, slots=bad.to(DEV), out=out0)
+        assert eng.sync_status() == q4.Q4_EINDEX
+        at = starts(new)
+        assert (out[at[1]:at[2]] == 3.0).all()
+        assert torch.equal(state[c.slots[1]].cpu(), c.state[c.slots[1]])
+        c.check(out, state, seqs=[0, 2])
+
+
+def test_linear_rows_of_no_sequence_and_graph(eng):
+    for new in ([1, 1], [100, 65]):
+        c = LinearCase(new, 1, 2, 64, 64, torch.float16, seed=26)
+        q, k, v = (torch.cat((x, torch.full_like(x[:2], float("nan")))) for x in (c.gq, c.gk, c.gv))
+        g = torch.cat((c.gg, c.gg[:2]))
+        out = torch.full((c.rows + 2, 2, 64), 3.0, dtype=torch.float16, device=DEV)
+        so = torch.zeros(3, 2, 64, 64, device=DEV)
+        s0, slots = c.state.to(DEV), c.slots.to(DEV)
+        call = lambda: eng.linattn(q, k, v, g, c.start, s0, state_out=so, slots=slots, out=out, max_new=max(new))  # noqa: E731
+        call()
+        assert eng.sync_status() == q4.Q4_OK
+        c.check(out[:c.rows], so)
+        assert (out[c.rows:] == 3.0).all()
+        first, fs = out.clone(), so.clone()
+        out.fill_(0)
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            call()
+        gr.replay()
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:c.rows], first[:c.rows]) and torch.equal(so, fs)
+
+
+# ---- refusals ---------------------------------------------------------------
+
+def test_refusals(eng):
+    c = AttendCase([2], [40], 4, 2, 64, 16, torch.float16, seed=30)
+    f = eng.rope_freqs(64)
+    q3 = c.gq
+
+    def refuses(status, call):
+        with pytest.raises(q4.Q4Error) as e:
+            call()
+        assert e.value.status == status, e.value
+
+    ap = lambda **kw: eng.attn_paged(c.cache, c.start, c.glen, kw.pop("q", q3), **kw)  # noqa: E731
+    refuses(q4.Q4_EINVAL, lambda: ap(out=q3))
+    refuses(q4.Q4_EINVAL, lambda: ap(window=-1))
+    refuses(q4.Q4_EINVAL, lambda: ap(max_new=0))
+    refuses(q4.Q4_EINVAL, lambda: ap(scale=float("nan")))
+    refuses(q4.Q4_EINVAL, lambda: ap(q=q3.float()))
+    refuses(q4.Q4_EINVAL, lambda: ap(q=q3.bfloat16()))
+    refuses(q4.Q4_EINVAL, lambda: ap(q=q3.cpu()))
+    refuses(q4.Q4_ESHAPE, lambda: ap(q=q3[:, :3].contiguous()))
+    refuses(q4.Q4_ESHAPE, lambda: ap(q=q3[..., :32]))
+    refuses(q4.Q4_ESHAPE, lambda: ap(out=torch.empty(3, 4, 64, dtype=torch.float16, device=DEV)))
+    refuses(q4.Q4_EALIGN, lambda: ap(q=torch.zeros(2 * 256 + 8, dtype=torch.float16, device=DEV)[1:513].view(2, 4, 64)))
+    refuses(q4.Q4_ESHAPE, lambda: ap(q=torch.zeros(2, 260, dtype=torch.float16, device=DEV)[:, :256].unflatten(1, (4, 64))))
+    refuses(q4.Q4_ESHAPE, lambda: eng.attn_paged(c.cache, c.start[:1], c.glen, q3))
+    refuses(q4.Q4_EINVAL, lambda: eng.attn_paged(c.cache, c.start.long(), c.glen, q3))
+    refuses(q4.Q4_ESHAPE, lambda: eng.attn_paged(c.cache, ints([0, 1, 2]), ints([1, 1]), q3))
+
+    k, v = c.cache.k, c.cache.v
+    refuses(q4.Q4_ESHAPE, lambda: q4.PagedKV(k, v[:, :8], c.cache.table))
+    refuses(q4.Q4_EINVAL, lambda: q4.PagedKV(k.float(), v.float(), c.cache.table))
+    refuses(q4.Q4_ESHAPE, lambda: q4.PagedKV(k, v, c.cache.table.long()))
+    refuses(q4.Q4_ESHAPE, lambda: q4.PagedKV(k.transpose(2, 3), v.transpose(2, 3), c.cache.table))
+    odd = torch.zeros(4, 16, 2, 20, dtype=torch.float16, device=DEV)
+    refuses(q4.Q4_ESHAPE, lambda: eng.attn_paged(q4.PagedKV(odd, odd.clone(), c.cache.table), c.start, c.glen,
+                                                 torch.zeros(2, 4, 20, dtype=torch.float16, device=DEV)))
+
+    nk = torch.zeros(2, 2, 64, dtype=torch.float16, device=DEV)
+    apd = lambda **kw: eng.kv_append(c.cache, c.start, c.glen, kw.pop("k", nk), kw.pop("v", nk), **kw)  # noqa: E731
+    refuses(q4.Q4_ESHAPE, lambda: apd(freqs=eng.rope_freqs(128)))
+    refuses(q4.Q4_EINVAL, lambda: apd(freqs=f.float()))
+    refuses(q4.Q4_EINVAL, lambda: apd(freqs=f, amp=float("inf")))
+    refuses(q4.Q4_ESHAPE, lambda: apd(v=nk[:1]))
+    refuses(q4.Q4_ESHAPE, lambda: apd(k=nk[:, :1]))
+    refuses(q4.Q4_ESHAPE, lambda: apd(pos=ints([1])))
+    refuses(q4.Q4_EINVAL, lambda: apd(q=q3, q_out=q3.bfloat16()))
+
+    lc = LinearCase([2], 1, 2, 64, 64, torch.float16, seed=31)
+    s = lc.state.to(DEV)
+    la = lambda **kw: eng.linattn(kw.pop("q", lc.gq), kw.pop("k", lc.gk), kw.pop("v", lc.gv),  # noqa: E731
+                                  kw.pop("g", lc.gg), lc.start, kw.pop("state", s), **kw)
+    refuses(q4.Q4_EINVAL, lambda: la(state=None))
+    refuses(q4.Q4_ESHAPE, lambda: la(state=s[:, :1]))
+    refuses(q4.Q4_ESHAPE, lambda: la(state=s.half()))
+    refuses(q4.Q4_ESHAPE, lambda: la(state_out=s.transpose(2, 3)))
+    refuses(q4.Q4_ESHAPE, lambda: la(g=lc.gg.half()))
+    refuses(q4.Q4_ESHAPE, lambda: la(g=lc.gg[:, :1]))
+    refuses(q4.Q4_EINVAL, lambda: la(k=lc.gk.bfloat16()))
+    refuses(q4.Q4_ESHAPE, lambda: la(k=lc.gk[:1]))
+    refuses(q4.Q4_EINVAL, lambda: la(scale=float("inf")))
+    refuses(q4.Q4_EINVAL, lambda: la(max_new=0))
+    refuses(q4.Q4_EINVAL, lambda: la(out=lc.gv))
+    refuses(q4.Q4_ESHAPE, lambda: la(slots=ints([0, 1])))
+    refuses(q4.Q4_ESHAPE, lambda: eng.linattn(lc.gq, lc.gk, lc.gv, lc.gg, ints([0, 1, 2]), s[:1]))
+    assert eng.sync_status() == q4.Q4_OK
+
+
+def test_fault_injection_reaches_these_calls(eng):
+    c = AttendCase([1], [20], 2, 1, 64, 16, torch.float16, seed=32)
+    lc = LinearCase([1], 1, 1, 64, 64, torch.float16, seed=32)
+    eng.set_fault("launch")
+    try:
+        for call in (lambda: c.run(eng), lambda: lc.run(eng),
+                     lambda: eng.kv_append(c.cache, c.start, c.glen, c.gq[:, :1], c.gq[:, 1:])):
+            with pytest.raises(q4.Q4Error) as e:
+                call()
+            assert e.value.status == q4.Q4_EFAULTINJ
+    finally:
+        eng.set_fault("none")
+    c.check(c.run(eng))
+
+
+def test_empty_batches(eng):
+    c = AttendCase([1], [20], 2, 1, 64, 16, torch.float16, seed=33)
+    none = c.gq[:0]
+    assert eng.attn_paged(c.cache, ints([0, 0]), ints([5]), none).shape == (0, 2, 64)
+    assert eng.attn_paged(c.cache, ints([0]), ints([]), none).shape == (0, 2, 64)
+    eng.kv_append(c.cache, ints([0, 0]), ints([5]), none[:, :1], none[:, :1])
+    lc = LinearCase([1], 1, 1, 64, 64, torch.float16, seed=33)
+    s0 = lc.state.to(DEV)
+    so = torch.zeros_like(s0)
+    out, _ = eng.linattn(lc.gq[:0], lc.gk[:0], lc.gv[:0], lc.gg[:0], ints([0, 0]), s0, state_out=so)
+    assert out.shape == (0, 1, 64)
+    assert torch.equal(so[0], s0[0]) and (so[1] == 0).all()      # a sequence without tokens copies its state
+    assert eng.sync_status() == q4.Q4_OK
+
+
+def test_streams(eng):
+    """Inputs made on one stream, the calls on another, the default left alone."""
+    side = torch.cuda.Stream()
+    c = AttendCase([1, 40], [200, 60], 4, 2, 128, 16, torch.float16, seed=34)
+    side.wait_stream(torch.cuda.current_stream())
+    out = c.run(eng, max_new=40, stream=side)
+    out2 = c.run(eng, max_new=40, stream=side.cuda_stream)
+    assert eng.sync_status(side) == q4.Q4_OK
+    c.check(out)
+    assert torch.equal(out, out2)
+
+
+# ---- a run of them together -------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prompt_then_tokens(eng, dtype):
+    """A prompt in two ragged chunks, then tokens one at a time: append and
+    attend on one cache give what attention over the whole sequence gives."""
+    hq, hkv, dim, page = 4, 2, 64, 16
+    total = [90, 41]
+    steps = [[70, 30], [15, 9], [1, 1], [1, 0], [1, 1], [2, 0]]
+    gen = torch.Generator().manual_seed(40)
+    table, pool = ref.table_of(total, page, gen)
+    nan = lambda: torch.full((pool, page, hkv, dim), float("nan"), dtype=dtype, device=DEV)  # noqa: E731
+    cache = q4.PagedKV(nan(), nan(), table.to(DEV))
+    x = [torch.randn(t, (hq + 2 * hkv), dim, generator=gen).to(dtype) for t in total]
+    freqs = eng.rope_freqs(dim // 2, base=500.0)
+    done, outs = [0, 0], [[], []]
+    for new in steps:
+        rows = torch.cat([x[s][done[s]:done[s] + n] for s, n in enumerate(new)]).to(DEV)
+        done = [d + n for d, n in zip(done, new)]
+        start, length = ints(starts(new)), ints(done)
+        q = eng.kv_append(cache, start, length, rows[:, hq:hq + hkv], rows[:, hq + hkv:], q=rows[:, :hq], freqs=freqs)
+        o = eng.attn_paged(cache, start, length, q, max_new=max(new))
+        outs[0].append(o[:new[0]])
+        outs[1].append(o[new[0]:])
+    assert eng.sync_status() == q4.Q4_OK and done == total
+    u = ref.half_step(dtype)
+    for s, t in enumerate(total):
+        pos = torch.arange(t)
+        got = torch.cat(outs[s])
+        q, _ = ref.rotate(x[s][:, :hq], pos, freqs.cpu())
+        k, _ = ref.rotate(x[s][:, hq:hq + hkv], pos, freqs.cpu())
+        q, k = q.to(dtype), k.to(dtype)                  # as stored
+        for h in range(hq):
+            v = x[s][:, hq + hkv + h // 2]
+            o, a, mags = ref.attend(q[:, h], k[:, h // 2], v, 0, dim ** -0.5)
+            # a stored value off by one rounding the other way moves a score by 2 u mags
+            tol = (u + (2 * dim * 2.0 ** -23 + 8 * u) * mags[:, None] + 2.0 ** -18) * a + t * 2.0 ** -25 * 6 + \
+                u * o.abs() + ref.tiny(dtype)
+            close(got[:, h], o, tol, f"sequence {s}, head {h}")
