@@ -19,17 +19,25 @@ struct AttnArgs {
     int q_heads, group;             // query heads, query heads of a key head
     float scale_log2;               // scale * log2(e): the softmax runs on powers of two
     int causal, window;             // window 0: none
+    int cap;                        // tokens that a row of the page table can hold
     int* err;
 };
 
-// Tokens [lo, hi) that new token t of a sequence (n new of len) sees.
+// Tokens [lo, hi) that new token t of a sequence (n new of len) sees.  Tokens
+// past the page table's columns are left out and reported.
 __device__ __forceinline__ void seen_range(const AttnArgs& a, int len, int n, int t, int& lo, int& hi) {
-    const int p = len - n + t;
-    hi = a.causal ? p + 1 : len;
-    lo = a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0;
-    if (hi < 0) hi = 0;
-    if (hi > len) hi = len;
-    if (lo > hi) lo = hi;
+    const int64_t p = (int64_t)len - n + t;
+    int64_t h = a.causal ? p + 1 : len;
+    if (h > a.cap) {
+        set_device_error(a.err, kDevIndex);
+        h = a.cap;
+    }
+    int64_t l = a.window > 0 ? p - a.window + 1 : 0;
+    if (h < 0) h = 0;
+    if (l < 0) l = 0;
+    if (l > h) l = h;
+    lo = (int)l;
+    hi = (int)h;
 }
 
 __device__ __forceinline__ float warp_xor_max(float v, int from) {
@@ -96,24 +104,6 @@ __device__ void attend_row(const AttnArgs& a, int s, int64_t r, int h, int lo, i
     if (on && grp == 0)
         *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + r * a.o_stride + (int64_t)h * a.kv.head_dim + 8 * c) =
             pack8<T>(y);
-}
-
-constexpr int kAttnRowWarps = 4;
-
-template <typename T>
-__global__ void __launch_bounds__(32 * kAttnRowWarps) attn_rows_kernel(const AttnArgs a) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t r = blockIdx.x;
-    const int h = blockIdx.y * kAttnRowWarps + (threadIdx.x >> 5);
-    if (h >= a.q_heads) return;
-    const int s = find_seq(a.batch.start, a.batch.n_seqs, r);
-    if (s < 0) return;
-    int64_t first;
-    int n, lo, hi;
-    seq_rows(a.batch, s, first, n);
-    seen_range(a, a.batch.len[s], n, (int)(r - first), lo, hi);
-    attend_row<T>(a, s, r, h, lo, hi);
 }
 
 }  // namespace q4

@@ -2,11 +2,12 @@
 // include/q4gemv.h): argument validation, kernel selection and launch.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
 #include "../../include/q4gemv.h"
-#include "attn_rows.cuh"
+#include "attn_split.cuh"
 #include "ctx_view.h"
 #include "kv_append.cuh"
 #include "linattn.cuh"
@@ -123,6 +124,25 @@ q4::RaggedArgs ragged(int64_t rows, int64_t n_seqs, const int32_t* start, const 
     return b;
 }
 
+int split_dp(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+
+template <typename T, int DP>
+cudaError_t split_launch_dp(const q4::SplitAttnArgs& g, int sms, cudaStream_t st) {
+    return launch(q4::attn_split_kernel<T, DP>, dim3((unsigned)(sms * q4::split_ctas_per_sm(DP))), q4::kSplitThreads,
+                  q4::split_smem(DP), st, g);
+}
+template <typename T>
+cudaError_t split_launch(const q4::SplitAttnArgs& g, int sms, cudaStream_t st) {
+    const int dp = split_dp(g.a.kv.head_dim);
+    return dp == 64 ? split_launch_dp<T, 64>(g, sms, st)
+                    : dp == 128 ? split_launch_dp<T, 128>(g, sms, st) : split_launch_dp<T, 256>(g, sms, st);
+}
+template <typename T, int DP>
+cudaError_t split_setup() {
+    return cudaFuncSetAttribute(q4::attn_split_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                q4::split_smem(DP));
+}
+
 template <typename T>
 cudaError_t append_launch(const q4::AppendArgs& a, bool interleaved, dim3 grid, cudaStream_t st) {
     if (interleaved)
@@ -132,6 +152,26 @@ cudaError_t append_launch(const q4::AppendArgs& a, bool interleaved, dim3 grid, 
 }
 
 }  // namespace
+
+cudaError_t q4::mix_setup() {
+    cudaError_t e = cudaSuccess;
+    for (cudaError_t r : {split_setup<__half, 64>(), split_setup<__half, 128>(), split_setup<__half, 256>(),
+                          split_setup<__nv_bfloat16, 64>(), split_setup<__nv_bfloat16, 128>(),
+                          split_setup<__nv_bfloat16, 256>()})
+        if (r != cudaSuccess) e = r;
+    return e;
+}
+
+void q4::mix_workspace(int sms, size_t* ws_bytes, size_t* cnt_bytes) {
+    size_t floats = 0, ctas = 0;
+    for (int dp : {64, 128, 256}) {
+        const size_t n = (size_t)sms * q4::split_ctas_per_sm(dp);
+        floats = std::max(floats, 2 * n * q4::split_slot(dp));
+        ctas = std::max(ctas, n);
+    }
+    *ws_bytes = floats * sizeof(float);
+    *cnt_bytes = ctas * sizeof(int);
+}
 
 extern "C" {
 
@@ -255,13 +295,17 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
     a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
     a.causal = causal ? 1 : 0;
     a.window = window > INT32_MAX ? INT32_MAX : (int)window;
+    a.cap = (int)std::min<int64_t>(kv->table_cols * kv->page_size, INT32_MAX - 4096);
     a.err = cx.err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 grid((unsigned)rows, (unsigned)((q_heads + q4::kAttnRowWarps - 1) / q4::kAttnRowWarps));
-    return launch_status(h, kv->dtype == Q4GEMV_F16
-                                ? launch(q4::attn_rows_kernel<__half>, grid, 32 * q4::kAttnRowWarps, 0, st, a)
-                                : launch(q4::attn_rows_kernel<__nv_bfloat16>, grid, 32 * q4::kAttnRowWarps, 0, st, a),
-                         call);
+    q4::SplitAttnArgs g;
+    g.a = a;
+    g.ws = cx.attn_ws;
+    g.cnt = cx.attn_cnt;
+    g.max_rows = 0;
+    g.min_blocks = 2;
+    return launch_status(h, kv->dtype == Q4GEMV_F16 ? split_launch<__half>(g, cx.sms, st)
+                                                    : split_launch<__nv_bfloat16>(g, cx.sms, st), call);
 }
 
 }  // extern "C"

@@ -15,6 +15,7 @@ template <typename T>
 struct Elem;
 template <>
 struct Elem<__half> {
+    static constexpr uint32_t kExpMask = 0x7C00u;   // all ones: infinity or NaN
     static __device__ __forceinline__ float2 unpack(uint32_t v) {
         return __half22float2(*reinterpret_cast<const __half2*>(&v));
     }
@@ -27,6 +28,7 @@ struct Elem<__half> {
 };
 template <>
 struct Elem<__nv_bfloat16> {
+    static constexpr uint32_t kExpMask = 0x7F80u;
     static __device__ __forceinline__ float2 unpack(uint32_t v) {
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
     }

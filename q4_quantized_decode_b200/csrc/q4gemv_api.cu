@@ -126,6 +126,8 @@ struct q4gemv_ctx {
     float* yacc = nullptr;           // fp32 panel sums of wide tensor-core GEMVs
     size_t yacc_floats = 0;
     __half* hio = nullptr;           // device copies of host x_in / x_out of run_stack
+    float* attn_ws = nullptr;        // shared pieces of the paged attention, and their counts
+    int* attn_cnt = nullptr;
     uint8_t* ximg = nullptr;         // activation image of the tensor-core GEMM
     size_t ximg_bytes = 0;
     int64_t hio_elems = 0;           // per vector
@@ -774,19 +776,23 @@ int q4gemv_create(q4gemv_t* out, int device) {
     const int f = parse_fault(getenv("Q4GEMV_FAULT"));
     h->fault = f < 0 ? kFaultNone : f;
     int rc = Q4_OK;
+    size_t attn_ws_bytes = 0, attn_cnt_bytes = 0;
     cudaError_t e = cudaSetDevice(device);
     if (e != cudaSuccess) rc = cuda_fail(h, e, "cudaSetDevice");
     if (rc == Q4_OK && h->fault == kFaultAlloc) rc = fail(h, Q4_EFAULTINJ, "injected allocation failure");
     if (rc == Q4_OK) {
         h->ws_warps = h->sms * kWarps;
         const size_t ws_bytes = (size_t)h->ws_warps * 2 * Q4GEMV_MAX_M_GEMV * 32 * sizeof(float);
+        q4::mix_workspace(h->sms, &attn_ws_bytes, &attn_cnt_bytes);
         if (cudaMalloc(&h->ws, ws_bytes) != cudaSuccess ||
             cudaMalloc(&h->cnt, (size_t)kMaxTiles * sizeof(int)) != cudaSuccess ||
             cudaMalloc(&h->err, sizeof(int)) != cudaSuccess ||
             cudaMalloc(&h->sync, 4 * sizeof(int)) != cudaSuccess ||
             cudaMalloc(&h->xq, 2 * q4::stack_xq_half_bytes(kStackKmax)) != cudaSuccess ||
             cudaMalloc(&h->yacc, kYaccPrealloc * sizeof(float)) != cudaSuccess ||
-            cudaMalloc(&h->ximg, kXimgPrealloc) != cudaSuccess)
+            cudaMalloc(&h->ximg, kXimgPrealloc) != cudaSuccess ||
+            cudaMalloc(&h->attn_ws, attn_ws_bytes) != cudaSuccess ||
+            cudaMalloc(&h->attn_cnt, attn_cnt_bytes) != cudaSuccess)
             rc = fail(h, Q4_ENOMEM, "workspace allocation failed");
         else {
             h->yacc_floats = kYaccPrealloc;
@@ -800,7 +806,8 @@ int q4gemv_create(q4gemv_t* out, int device) {
     }
     if (rc == Q4_OK) {
         if (cudaMemset(h->cnt, 0, (size_t)kMaxTiles * sizeof(int)) != cudaSuccess ||
-            cudaMemset(h->err, 0, sizeof(int)) != cudaSuccess)
+            cudaMemset(h->err, 0, sizeof(int)) != cudaSuccess ||
+            cudaMemset(h->attn_cnt, 0, attn_cnt_bytes) != cudaSuccess)
             rc = fail(h, Q4_ECUDA, "workspace initialisation failed");
     }
     if (rc == Q4_OK) {
@@ -815,7 +822,7 @@ int q4gemv_create(q4gemv_t* out, int device) {
             set_smem_attr(q4::gemm_tc_kernel<false, true>) ||
             set_smem_attr(q4::gemm_tc_kernel<true, true>) ||
             set_smem_attr(q4::gemv_tcs_kernel<8>) || set_smem_attr(q4::gemv_tcs_kernel<16>) ||
-            0)
+            q4::mix_setup() != cudaSuccess)
             rc = fail(h, Q4_ECUDA, "cudaFuncSetAttribute failed");
     }
     if (rc == Q4_OK) {
@@ -834,6 +841,8 @@ int q4gemv_create(q4gemv_t* out, int device) {
         cudaFree(h->xq);
         cudaFree(h->yacc);
         cudaFree(h->ximg);
+        cudaFree(h->attn_ws);
+        cudaFree(h->attn_cnt);
         if (h->cap) cudaStreamDestroy(h->cap);
         delete h;
         return rc;
@@ -858,6 +867,8 @@ int q4gemv_destroy(q4gemv_t h) {
     cudaFree(h->yacc);
     cudaFree(h->hio);
     cudaFree(h->ximg);
+    cudaFree(h->attn_ws);
+    cudaFree(h->attn_cnt);
     cudaFree(h->gscr);
     shard_release(h);
     peer_release(h);
@@ -1660,6 +1671,8 @@ q4::CtxView q4::ctx_view(q4gemv_t h) {
     v.sms = h->sms;
     v.fail_launch = h->fault == kFaultLaunch;
     v.err = h->err;
+    v.attn_ws = h->attn_ws;
+    v.attn_cnt = h->attn_cnt;
     return v;
 }
 
