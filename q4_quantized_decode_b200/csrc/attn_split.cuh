@@ -442,28 +442,52 @@ __global__ void __launch_bounds__(kSplitThreads, split_ctas_per_sm(DP)) attn_spl
             if (last_word) {
                 __threadfence();
                 if (threadIdx.x == 0) g.cnt[c_lo] = 0;
-                auto piece = [&](int p) {
-                    const int64_t c = c_lo + p;
-                    return g.ws + (2 * c + (run_start(c) >= ub ? 0 : 1)) * split_slot(DP);
-                };
+                // Shared memory: each piece's slot, its rows' weights
+                // [pieces][16], the rows' 1 / sum.
+                int* slots = reinterpret_cast<int*>(split_smem_raw);
+                float* wts = reinterpret_cast<float*>(slots + gridDim.x);
+                float* invs = wts + gridDim.x * kSplitRows;
+                for (int p = threadIdx.x; p < pieces; p += kSplitThreads)
+                    slots[p] = (int)(2 * (c_lo + p) + (run_start(c_lo + p) >= ub ? 0 : 1));
+                __syncthreads();
+                {
+                    // Eight threads a row.
+                    const int row = threadIdx.x >> 3, part = threadIdx.x & 7;
+                    float mx = -INFINITY, ls = 0.f;
+                    if (row < n_rows)
+                        for (int p = part; p < pieces; p += 8) {
+                            const float v = __ldcg(g.ws + (int64_t)slots[p] * split_slot(DP) + kSplitRows * DP + row);
+                            wts[p * kSplitRows + row] = v;
+                            mx = fmaxf(mx, v);
+                        }
+#pragma unroll
+                    for (int x = 1; x < 8; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+                    const float mu = mx == -INFINITY ? 0.f : mx;
+                    if (row < n_rows)
+                        for (int p = part; p < pieces; p += 8) {
+                            const float wt = exp2f(wts[p * kSplitRows + row] - mu);
+                            wts[p * kSplitRows + row] = wt;
+                            ls += wt * __ldcg(g.ws + (int64_t)slots[p] * split_slot(DP) + kSplitRows * DP + kSplitRows + row);
+                        }
+#pragma unroll
+                    for (int x = 1; x < 8; x <<= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, x);
+                    if (part == 0) invs[row] = ls == 0.f ? 0.f : 1.f / ls;
+                }
+                __syncthreads();
                 for (int x = threadIdx.x; x < n_rows * (DP / 4); x += kSplitThreads) {
                     const int row = x / (DP / 4), c4 = x % (DP / 4);
-                    float mx = -INFINITY, ls = 0.f;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int p = 0; p < pieces; ++p) mx = fmaxf(mx, __ldcg(piece(p) + kSplitRows * DP + row));
-                    const float mu = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 4
+#pragma unroll 8
                     for (int p = 0; p < pieces; ++p) {
-                        const float* sp = piece(p);
-                        const float wt = exp2f(__ldcg(sp + kSplitRows * DP + row) - mu);
-                        const float4 u = __ldcg(reinterpret_cast<const float4*>(sp + row * DP + 4 * c4));
-                        ls += wt * __ldcg(sp + kSplitRows * DP + kSplitRows + row);
+                        const float wt = wts[p * kSplitRows + row];
+                        const float4 u = __ldcg(reinterpret_cast<const float4*>(g.ws + (int64_t)slots[p] * split_slot(DP) +
+                                                                                row * DP + 4 * c4));
                         v.x += wt * u.x;
                         v.y += wt * u.y;
                         v.z += wt * u.z;
                         v.w += wt * u.w;
                     }
-                    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+                    const float inv = invs[row];
                     store_out(row, c4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 }
             }

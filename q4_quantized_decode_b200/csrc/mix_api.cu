@@ -10,7 +10,7 @@
 #include "attn_split.cuh"
 #include "ctx_view.h"
 #include "kv_append.cuh"
-#include "linattn.cuh"
+#include "lin_chunk.cuh"
 
 namespace {
 
@@ -124,6 +124,9 @@ q4::RaggedArgs ragged(int64_t rows, int64_t n_seqs, const int32_t* start, const 
     return b;
 }
 
+// Up to this many new tokens of a sequence run token by token.
+constexpr int kLinRecurMax = 8;
+
 int split_dp(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 template <typename T, int DP>
@@ -143,6 +146,20 @@ cudaError_t split_setup() {
                                 q4::split_smem(DP));
 }
 
+template <typename T, int DK, int MT>
+cudaError_t chunk_setup() {
+    return cudaFuncSetAttribute(q4::lin_chunk_kernel<T, DK, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                q4::lc_smem(DK, MT));
+}
+template <typename T>
+cudaError_t setup_type() {
+    for (cudaError_t e : {split_setup<T, 64>(), split_setup<T, 128>(), split_setup<T, 256>(), chunk_setup<T, 64, 1>(),
+                          chunk_setup<T, 64, 2>(), chunk_setup<T, 128, 1>(), chunk_setup<T, 128, 2>(),
+                          chunk_setup<T, 256, 1>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
+}
+
 template <typename T>
 cudaError_t append_launch(const q4::AppendArgs& a, bool interleaved, dim3 grid, cudaStream_t st) {
     if (interleaved)
@@ -154,12 +171,8 @@ cudaError_t append_launch(const q4::AppendArgs& a, bool interleaved, dim3 grid, 
 }  // namespace
 
 cudaError_t q4::mix_setup() {
-    cudaError_t e = cudaSuccess;
-    for (cudaError_t r : {split_setup<__half, 64>(), split_setup<__half, 128>(), split_setup<__half, 256>(),
-                          split_setup<__nv_bfloat16, 64>(), split_setup<__nv_bfloat16, 128>(),
-                          split_setup<__nv_bfloat16, 256>()})
-        if (r != cudaSuccess) e = r;
-    return e;
+    const cudaError_t e = setup_type<__half>();
+    return e != cudaSuccess ? e : setup_type<__nv_bfloat16>();
 }
 
 void q4::mix_workspace(int sms, size_t* ws_bytes, size_t* cnt_bytes) {
@@ -313,11 +326,28 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
 namespace {
 
 template <typename T>
-cudaError_t linattn_launch(const q4::LinArgs& a, cudaStream_t st) {
+cudaError_t lin_recur_launch(const q4::LinArgs& a, cudaStream_t st) {
     const dim3 grid((unsigned)a.n_seqs, (unsigned)a.v_heads, (unsigned)((a.v_dim + q4::kLinCols - 1) / q4::kLinCols));
     if (a.k_dim <= 64) return launch(q4::lin_recur_kernel<T, 4>, grid, q4::kLinThreads, 0, st, a);
     if (a.k_dim <= 128) return launch(q4::lin_recur_kernel<T, 8>, grid, q4::kLinThreads, 0, st, a);
     return launch(q4::lin_recur_kernel<T, 16>, grid, q4::kLinThreads, 0, st, a);
+}
+
+template <typename T, int DK, int MT>
+cudaError_t lin_chunk_launch(const q4::LinArgs& a, cudaStream_t st) {
+    const dim3 grid((unsigned)a.v_heads, (unsigned)((a.v_dim + q4::lc_cols(MT) - 1) / q4::lc_cols(MT)),
+                    (unsigned)a.n_seqs);
+    return launch(q4::lin_chunk_kernel<T, DK, MT>, grid, q4::kLcThreads, q4::lc_smem(DK, MT), st, a);
+}
+
+// Prompts run in chunks; a warp takes 32 value columns (half the shared-memory
+// reads of a product) where that leaves two CTAs for every SM, 16 otherwise.
+template <typename T>
+cudaError_t lin_prompt_launch(const q4::LinArgs& a, int sms, cudaStream_t st) {
+    const bool wide = a.v_dim > 64 && (int64_t)a.n_seqs * a.v_heads * ((a.v_dim + 127) / 128) >= 2 * (int64_t)sms;
+    if (a.k_dim <= 64) return wide ? lin_chunk_launch<T, 64, 2>(a, st) : lin_chunk_launch<T, 64, 1>(a, st);
+    if (a.k_dim <= 128) return wide ? lin_chunk_launch<T, 128, 2>(a, st) : lin_chunk_launch<T, 128, 1>(a, st);
+    return lin_chunk_launch<T, 256, 1>(a, st);
 }
 
 }  // namespace
@@ -380,6 +410,9 @@ extern "C" int q4gemv_linattn(q4gemv_t h, const q4gemv_linattn_args* args, int64
     a.scale = p.scale;
     a.err = cx.err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return launch_status(h, p.dtype == Q4GEMV_F16 ? linattn_launch<__half>(a, st) : linattn_launch<__nv_bfloat16>(a, st),
-                         call);
+    const bool f16 = p.dtype == Q4GEMV_F16;
+    if (max_new <= kLinRecurMax)
+        return launch_status(h, f16 ? lin_recur_launch<__half>(a, st) : lin_recur_launch<__nv_bfloat16>(a, st), call);
+    return launch_status(h, f16 ? lin_prompt_launch<__half>(a, cx.sms, st)
+                                : lin_prompt_launch<__nv_bfloat16>(a, cx.sms, st), call);
 }

@@ -529,6 +529,68 @@ def test_linear_strong_and_weak_decays(eng, rate):
         c.check(out, state)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kq,vv", [(2.0 ** -12, 1.0), (200.0, 100.0), (2.0 ** -6, 2.0 ** -9), (30.0, 2.0 ** -10)])
+def test_linear_magnitudes(eng, dtype, kq, vv):
+    """Keys, queries and values far from 1, and changing from chunk to chunk:
+    the state keeps 32 bits' worth and nothing overflows on the way."""
+    c = LinearCase([200, 5], 1, 2, 64, 64, dtype, seed=27)
+    grow = torch.ones(c.rows, 1, 1)
+    grow[64:128] = 8.0
+    grow[128:] = 0.25
+    c.q, c.k, c.v = (c.q.float() * 8 * kq).to(dtype), (c.k.float() * 8 * kq * grow).to(dtype), (c.v.float() * vv).to(dtype)
+    c.state = c.state * (kq * vv)
+    c.gq, c.gk, c.gv = c.q.to(DEV), c.k.to(DEV), c.v.to(DEV)
+    scale = 1.0 / (kq * kq * vv * 64)                    # outputs inside the type's range
+    out, state = c.run(eng, scale=scale)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(out, state, scale=scale)
+
+
+def test_linear_values_past_the_tensor_range(eng):
+    """bfloat16 magnitudes of 2^35 in one chunk (run token by token), ordinary
+    ones before and behind."""
+    c = LinearCase([200], 1, 1, 64, 128, torch.bfloat16, seed=28)
+    big = torch.ones(c.rows, 1, 1)
+    big[70:75] = 2.0 ** 35
+    c.v = (c.v.float() * big).to(torch.bfloat16)
+    c.gv = c.v.to(DEV)
+    out, state = c.run(eng)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(out, state)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", ["q", "k", "v", "g"])
+def test_linear_non_finite_tokens_reach_only_later_rows(eng, bad, what):
+    if what == "g" and bad > 0:
+        bad = float("nan")
+    c = LinearCase([150, 20], 1, 2, 64, 64, torch.float16, seed=29)
+    out0, state0 = c.run(eng)
+    x = {"q": c.gq, "k": c.gk, "v": c.gv, "g": c.gg}[what].clone()
+    if what == "g":
+        x[100, 0] = bad
+        c.gg = x
+    else:
+        x[100, 0, 5] = bad
+        setattr(c, "g" + what, x)
+    out, state = c.run(eng)
+    assert eng.sync_status() == q4.Q4_OK
+    clean = out0.clone()
+    clean[:100] = out[:100]
+    clean[150:] = out[150:]
+    clean[:, 1] = out[:, 1] if what in ("v", "g") else clean[:, 1]      # the other value head
+    c.check(clean, state0)
+    hit = out[100:150, 0, 5] if what == "v" else out[100:150, 0]
+    assert not torch.isfinite(out[100, 0]).all()
+    if what != "q":
+        assert not torch.isfinite(hit).any()
+    else:
+        keep = out.clone()
+        keep[100] = out0[100]
+        c.check(keep, state)
+
+
 def test_linear_decay_of_minus_infinity_clears(eng):
     for new in ([3], [150]):
         c = LinearCase(new, 1, 1, 64, 64, torch.float16, seed=22)
