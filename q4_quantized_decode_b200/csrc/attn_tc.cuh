@@ -1,0 +1,799 @@
+// Attention of many new tokens (chunks of prompts) over a paged cache on the
+// 5th-generation tensor cores.
+//
+// The rows of a sequence (its new tokens times the query heads of one key
+// head) form tiles of 256, two accumulators of 128: a tile of one key head is
+// a unit.  For every 128 keys a CTA computes S = Q K^T of both accumulators,
+// turns S into weights P = 2^(S - m) and adds P V to both sums:
+//   warps 0-3, 4-7  the softmax of one accumulator each, a thread a row: S from
+//              tensor memory, the running maximum m and sum (32 bits), P back
+//              into S's place in the 16-bit type (the one rounding before the
+//              output's), the sums brought to a new m when it has risen by more
+//              than 2^8 (until then P may pass 1 and stays far from overflow);
+//   warp 8     one thread issues the products: S of one accumulator runs while
+//              the other one's softmax does;
+//   warps 9-11 the pages' rows into a ring of 128-key tiles (asynchronous
+//              16-byte copies, because pages end anywhere in a tile; keys that
+//              no row sees are zeros), in the 128-byte swizzle that the
+//              products read: K as rows of K, V as an N-major operand.
+// Two products of 128 x 128 x head_dim for each accumulator and tile, 16384
+// powers of two: the tensor pipe and the exponential unit need about the same
+// time, 2048 cycles for a CTA's tile at head size 128, and bound this together.
+//
+// The units' key tiles are cut over the CTAs on the device: with few units
+// each is split over several CTAs, with many the units' costs (which grow with
+// the rows' places, when causal) form one line that is cut into equal runs.
+// Pieces of a unit go to the workspace, at most two a CTA, and the CTA that
+// comes last joins them in order.
+//
+// What rows do not see cannot reach them: a weight of zero times a value that
+// is not finite would (and a page outside the pool has no keys at all), so the
+// copying warps look at values in tiles that rows see in different parts, and
+// a unit with such a value, or with a bad page, is taken row by row at the end.
+#pragma once
+
+#include "attn_rows.cuh"
+#include "mma_common.cuh"
+#include "tc_common.cuh"
+
+namespace q4 {
+
+constexpr int kTaRows = 256;                 // rows of a unit
+constexpr int kTaKeys = 128;                 // keys of a tile
+constexpr int kTaLoaders = 3;
+constexpr int kTaThreads = 32 * (8 + 1 + kTaLoaders);
+constexpr int kTaLag = 2;                    // copies in flight behind the newest
+constexpr int kTaOver = 128;                 // a unit's fixed cost in keys: its start and end
+
+// Ring slots (a K or a V tile each) beside the queries.
+__host__ __device__ constexpr int ta_slots(int dp) { return dp == 64 ? 8 : 4; }
+__host__ __device__ constexpr int ta_smem(int dp) {
+    return 1024 + kTaRows * dp * 2 + ta_slots(dp) * kTaKeys * dp * 2 + 512;
+}
+// Floats of a workspace slot: sums [dp / 4][256][4], maxima, weights' sums.
+__host__ __device__ constexpr int ta_slot(int dp) { return kTaRows * (dp + 2); }
+
+struct TcAttnArgs {
+    AttnArgs a;
+    float* ws;           // [2 * gridDim.x] slots
+    int* cnt;            // [gridDim.x] arrivals, zero between calls
+    int min_rows;        // sequences of at most this many rows are another kernel's
+    int min_cost;        // keys of a run, at least
+    uint32_t idesc_s, idesc_o;
+};
+
+// The units of a sequence: `tiles` row tiles, of cost c0 + c1 rt each.
+struct TaSeq {
+    int64_t first;
+    int n, len, tiles, c0, c1;
+    __device__ __forceinline__ int64_t before(int64_t rt) const { return rt * c0 + c1 * (rt * (rt - 1) / 2); }
+};
+
+__device__ __forceinline__ TaSeq ta_seq(const TcAttnArgs& g, int s) {
+    TaSeq q;
+    seq_rows(g.a.batch, s, q.first, q.n);
+    q.len = g.a.batch.len[s];
+    const int64_t rows = (int64_t)q.n * g.a.group;
+    q.tiles = q.c0 = q.c1 = 0;
+    if (rows <= g.min_rows) return q;
+    q.tiles = (int)((rows + kTaRows - 1) / kTaRows);
+    int lo, hi;
+    if (g.a.causal && (g.a.window == 0 || g.a.window >= q.len)) {
+        seen_range(g.a, q.len, q.n, min(q.n - 1, (kTaRows - 1) / g.a.group), lo, hi);
+        q.c1 = kTaRows / g.a.group;
+    } else {
+        seen_range(g.a, q.len, q.n, q.n - 1, lo, hi);
+    }
+    q.c0 = hi - lo + kTaOver;
+    return q;
+}
+
+// A CTA's part of one unit.
+struct TaSeg {
+    int s, rt, hk;
+    int64_t first;
+    int n, len;
+    int j0;              // first key of the piece, a multiple of 128 over the pages
+    int nt;              // its 128-key tiles
+    int tlo, thi;        // keys that any row of the unit sees
+    int pieces;          // pieces of the unit
+    int64_t c_lo;        // CTA of the first piece
+    int64_t ub;          // the unit's place on the cost line
+    int slot;            // 0: this CTA's first workspace slot, 1: its second
+};
+
+// Walks over a CTA's units; every warp does it for itself.
+struct TaWalk {
+    int64_t total, runs, b, b1, b0, seq_base;
+    int s, k;            // k > 0: few units, k CTAs for each
+    TaSeq q;
+    bool done;
+};
+
+__device__ __forceinline__ int64_t ta_cut(int64_t total, int64_t runs, int64_t c) { return c * total / runs; }
+
+// The sequence whose units (by count, or by cost) hold place x.
+__device__ __forceinline__ void ta_find(const TcAttnArgs& g, int64_t x, bool by_units, int& s, int64_t& base) {
+    const int lane = threadIdx.x & 31, nh = g.a.kv.n_heads, n_seqs = g.a.batch.n_seqs;
+    base = 0;
+    s = 0;
+    for (int c0 = 0; c0 < n_seqs; c0 += 32) {
+        int64_t v = 0;
+        if (c0 + lane < n_seqs) {
+            const TaSeq q = ta_seq(g, c0 + lane);
+            v = (by_units ? q.tiles : q.before(q.tiles)) * nh;
+        }
+        int64_t p = v;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, p, d);
+            if (lane >= d) p += y;
+        }
+        const unsigned past = __ballot_sync(0xFFFFFFFFu, base + p > x);
+        if (past) {
+            const int l = __ffs((int)past) - 1;
+            s = c0 + l;
+            base += __shfl_sync(0xFFFFFFFFu, p - v, l);
+            return;
+        }
+        base += __shfl_sync(0xFFFFFFFFu, p, 31);
+    }
+}
+
+__device__ __forceinline__ TaWalk ta_start(const TcAttnArgs& g) {
+    TaWalk w;
+    const int lane = threadIdx.x & 31, nh = g.a.kv.n_heads, n_seqs = g.a.batch.n_seqs;
+    int64_t units = 0, cost = 0;
+    for (int s = lane; s < n_seqs; s += 32) {
+        const TaSeq q = ta_seq(g, s);
+        units += (int64_t)q.tiles * nh;
+        cost += q.before(q.tiles) * nh;
+    }
+    for (int x = 16; x; x >>= 1) {
+        units += __shfl_xor_sync(0xFFFFFFFFu, units, x);
+        cost += __shfl_xor_sync(0xFFFFFFFFu, cost, x);
+    }
+    w.total = cost;
+    w.done = units == 0;
+    w.k = 0;
+    w.b0 = w.b = w.b1 = 0;
+    if (w.done) return w;
+    const int64_t c = blockIdx.x;
+    if (2 * units <= (int64_t)gridDim.x) {
+        w.k = (int)(gridDim.x / units);
+        w.runs = 0;
+        const int64_t u = c / w.k;
+        w.done = u >= units;
+        if (w.done) return w;
+        ta_find(g, u, true, w.s, w.seq_base);
+        w.q = ta_seq(g, w.s);
+        w.b = u - w.seq_base;                 // the unit within the sequence
+        return w;
+    }
+    w.runs = min((int64_t)gridDim.x, max((int64_t)1, cost / g.min_cost));
+    w.done = c >= w.runs;
+    if (w.done) return w;
+    w.b0 = w.b = ta_cut(cost, w.runs, c);
+    w.b1 = ta_cut(cost, w.runs, c + 1);
+    ta_find(g, w.b, false, w.s, w.seq_base);
+    w.q = ta_seq(g, w.s);
+    return w;
+}
+
+// The next part of this CTA's run; false at its end.
+__device__ __forceinline__ bool ta_next(const TcAttnArgs& g, TaWalk& w, TaSeg& e) {
+    if (w.done) return false;
+    const int nh = g.a.kv.n_heads;
+    int64_t v0 = 0, v1 = 1, cu = 1;           // the piece within the unit's cost
+    if (w.k) {
+        e.rt = (int)(w.b / nh);
+        e.hk = (int)(w.b - (int64_t)e.rt * nh);
+        w.done = true;
+    } else {
+        if (w.b >= w.b1) return false;
+        while (w.b >= w.seq_base + w.q.before(w.q.tiles) * nh && w.s + 1 < g.a.batch.n_seqs) {
+            w.seq_base += w.q.before(w.q.tiles) * nh;
+            w.q = ta_seq(g, ++w.s);
+        }
+        // The row tile whose units hold the place: before(rt) <= x / nh.
+        const int64_t x = w.b - w.seq_base, xh = x / nh;
+        int64_t rt;
+        if (w.q.c1 == 0) {
+            rt = xh / max(1, w.q.c0);
+        } else {
+            const double c1 = w.q.c1, m = w.q.c0 - 0.5 * c1;
+            rt = (int64_t)((sqrt(m * m + 2.0 * c1 * (double)xh) - m) / c1);
+        }
+        rt = max((int64_t)0, min(rt, (int64_t)w.q.tiles - 1));
+        while (rt > 0 && w.q.before(rt) > xh) --rt;
+        while (rt + 1 < w.q.tiles && w.q.before(rt + 1) <= xh) ++rt;
+        cu = w.q.c0 + (int64_t)w.q.c1 * rt;
+        const int64_t in = x - w.q.before(rt) * nh;
+        e.rt = (int)rt;
+        e.hk = (int)(in / cu);
+        v0 = in - e.hk * cu;
+        e.ub = w.b - v0;
+        v1 = min(cu, v0 + (w.b1 - w.b));
+        e.slot = w.b == w.b0 ? 0 : 1;
+        w.b += v1 - v0;
+    }
+    e.s = w.s;
+    e.first = w.q.first;
+    e.n = w.q.n;
+    e.len = w.q.len;
+    // Keys of the unit: the first row starts lowest, the last ends highest.
+    const int t0 = (int)((int64_t)e.rt * kTaRows / g.a.group);
+    const int t1 = min(e.n - 1, (int)(((int64_t)(e.rt + 1) * kTaRows - 1) / g.a.group));
+    int lo1, hi0;
+    seen_range(g.a, e.len, e.n, t0, e.tlo, hi0);
+    seen_range(g.a, e.len, e.n, t1, lo1, e.thi);
+    const int base = e.tlo / kTaKeys * kTaKeys;
+    const int T = e.thi > e.tlo ? (e.thi - base + kTaKeys - 1) / kTaKeys : 0;
+    if (w.k) {
+        // As many pieces as leave a piece about as many tiles as there are
+        // pieces to join.
+        int k = 1;
+        while (k < w.k && (k + 1) * (k + 1) <= T) ++k;
+        const int p = (int)(blockIdx.x % (unsigned)w.k);
+        if (p >= k) return false;
+        v0 = p;
+        v1 = p + 1;
+        cu = k;
+        e.c_lo = (int64_t)blockIdx.x - p;
+        e.pieces = k;
+        e.slot = 0;
+        e.ub = 0;
+    } else if (v0 == 0 && v1 == cu) {
+        e.pieces = 1;
+        e.c_lo = blockIdx.x;
+    } else {
+        auto cta_of = [&](int64_t x) {
+            int64_t c = x * w.runs / w.total;
+            while (c + 1 < w.runs && ta_cut(w.total, w.runs, c + 1) <= x) ++c;
+            while (c > 0 && ta_cut(w.total, w.runs, c) > x) --c;
+            return c;
+        };
+        e.c_lo = cta_of(e.ub);
+        e.pieces = (int)(cta_of(e.ub + cu - 1) - e.c_lo) + 1;
+    }
+    const int i0 = (int)(T * v0 / cu), i1 = (int)(T * v1 / cu);
+    e.j0 = base + i0 * kTaKeys;
+    e.nt = i1 - i0;
+    return true;
+}
+
+// Workspace slot of piece p of a unit.
+__device__ __forceinline__ int64_t ta_piece(const TaWalk& w, const TaSeg& e, int p) {
+    const int64_t c = e.c_lo + p;
+    return 2 * c + (w.k == 0 && ta_cut(w.total, w.runs, c) < e.ub ? 1 : 0);
+}
+
+// A wait that gives up when another role has, or after about 20 seconds (the
+// longest that a role keeps others waiting in earnest is a unit taken row by
+// row, milliseconds for ordinary contexts).
+__device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 15) == 15 && (*abort_flag || clock64() - t0 > (1ll << 35))) return false;
+    }
+}
+
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const TcAttnArgs g) {
+    constexpr int NS = ta_slots(DP);
+    constexpr int CH = DP / 8;
+    constexpr uint32_t kHalf = kTaKeys * 128;            // one 64-element part of a 128-row tile
+    constexpr uint32_t kTile = kHalf * (DP / 64);
+    constexpr uint32_t kColO = 256;                      // TMEM columns: S at 0 and 128, sums from 256
+    extern __shared__ uint8_t ta_raw[];
+    const uint32_t raw0 = smem_addr(ta_raw);
+    const uint32_t sQ = (raw0 + 1023u) & ~1023u;         // two tiles of 128 rows
+    const uint32_t sRing = sQ + 2 * kTile;
+    uint64_t* full = reinterpret_cast<uint64_t*>(ta_raw + (sRing - raw0) + NS * kTile);   // [NS]
+    uint64_t* empty = full + NS;                         // [NS]
+    uint64_t* qfull = empty + NS;                        // queries in place
+    uint64_t* sfull = qfull + 1;                         // [2] S computed
+    uint64_t* pfull = sfull + 2;                         // [2] P written
+    uint64_t* ofull = pfull + 2;                         // [2] the piece's sums complete
+    uint64_t* idle = ofull + 2;                          // every product done
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(idle + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+    volatile int* never = abort_flag + 1;                // stays 0
+    volatile int* stop = abort_flag + 2;                 // the softmax warps' common end
+    volatile int* last_word = abort_flag + 3;
+    volatile int* odd = abort_flag + 4;                  // [16] of the pieces with keys, in order: take it row by row
+
+    const AttnArgs& a = g.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int D = a.kv.head_dim;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + i, kTaLoaders);
+            mbar_init(empty + i, 1);
+        }
+        mbar_init(qfull, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull + i, 1);
+            mbar_init(pfull + i, 4);
+            mbar_init(ofull + i, 1);
+        }
+        for (int i = 0; i < 16; ++i) odd[i] = 0;
+        mbar_init(idle, 1);
+        *abort_flag = *never = *stop = 0;
+        fence_barrier_init();
+    }
+    if (warp == 8) tc_alloc(tslot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // Each warp's walk and piece live in shared memory (all lanes write the
+    // same words): registers are for the softmax's rows.
+    __shared__ TaWalk walks[kTaThreads / 32];
+    __shared__ TaSeg segs[kTaThreads / 32];
+    TaWalk& w = walks[warp];
+    TaSeg& e = segs[warp];
+    w = ta_start(g);
+    __syncwarp();
+    auto next = [&]() {
+        TaWalk wn = w;
+        TaSeg en;
+        __syncwarp();
+        const bool more = ta_next(g, wn, en);
+        w = wn;
+        e = en;
+        __syncwarp();
+        return more;
+    };
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        set_device_error(a.err, kDevTimeout);
+    };
+
+    if (warp >= 8) {
+    if (warp > 8) {
+        // ---- copies ----
+        const int lw = warp - 9;
+        uint32_t u = 0;                                  // tiles begun
+        uint32_t told = 0;                               // tiles whose arrival was signalled
+        int64_t off[4];
+        uint32_t look = 0, mark = 0;                     // of the tiles in flight: V tiles to look over, their pieces
+        int seg_no = 0;
+        bool ok = true;
+        auto signal = [&](uint32_t upto) {
+            for (; told < upto; ++told) {
+                const uint32_t st = told % NS;
+                if (look >> (told & 7) & 1) {
+                    // this thread's own chunks of a V tile
+                    bool bad = false;
+                    const uint32_t vt = sRing + st * kTile;
+#pragma unroll
+                    for (int gq = 0; gq < 4; ++gq)
+                        for (int x = lw; x < 32 * CH / 32; x += kTaLoaders) {
+                            const int ci = x * 32 + lane, row = 32 * gq + ci / CH, ch = ci % CH;
+                            const uint4 v = lds128(vt + (uint32_t)(ch >> 3) * kHalf +
+                                                   (uint32_t)(row * 128 + (((ch & 7) ^ (row & 7)) << 4)));
+                            constexpr uint32_t ex = Elem<T>::kExpMask;
+                            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                bad |= (vw[y] & ex) == ex || (vw[y] & (ex << 16)) == (ex << 16);
+                        }
+                    if (bad) odd[(mark >> (4 * (told & 7))) & 15] = 1;
+                    look &= ~(1u << (told & 7));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + st);
+            }
+        };
+        while (ok && next()) {
+            const int64_t ho = (int64_t)e.hk * a.kv.head_stride;
+            // Keys that every row of the unit sees: tiles inside need no look.
+            const int t0 = (int)((int64_t)e.rt * kTaRows / a.group);
+            const int t1 = min(e.n - 1, (int)(((int64_t)(e.rt + 1) * kTaRows - 1) / a.group));
+            int ilo, ihi, x0;
+            seen_range(a, e.len, e.n, t1, ilo, x0);
+            seen_range(a, e.len, e.n, t0, x0, ihi);
+            for (int i = 0; i < e.nt && ok; ++i) {
+                const int j = e.j0 + i * kTaKeys;
+                bool page_bad = false;
+#pragma unroll
+                for (int gq = 0; gq < 4; ++gq) {
+                    const int key = j + 32 * gq + lane;
+                    off[gq] = -1;
+                    if (key >= e.tlo && key < e.thi) {
+                        off[gq] = token_offset(a.kv, e.s, key, a.err);
+                        if (off[gq] < 0) page_bad = true;
+                        else off[gq] += ho;
+                    }
+                }
+                if (page_bad) odd[seg_no & 15] = 1;
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++u) {
+                    const uint32_t st = u % NS;
+                    if (u >= NS) {
+                        const uint32_t par = ((u / NS) - 1) & 1;
+                        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(empty + st, par))) {
+                            cp_async_wait<0>();          // nothing more to begin: hand over what is there
+                            signal(u);
+                            ok = __all_sync(0xFFFFFFFFu, ta_wait(empty + st, par, abort_flag));
+                            if (!ok) break;
+                        }
+                    }
+                    const T* src = static_cast<const T*>(kv ? a.kv.v : a.kv.k);
+                    const uint32_t dst = sRing + st * kTile;
+#pragma unroll
+                    for (int gq = 0; gq < 4; ++gq)
+                        for (int x = lw; x < CH; x += kTaLoaders) {
+                            const int ci = x * 32 + lane, row = ci / CH, ch = ci % CH;
+                            const int64_t o = __shfl_sync(0xFFFFFFFFu, off[gq], row);
+                            const bool in = o >= 0 && 8 * ch < D;
+                            const int rr = 32 * gq + row;
+                            cp_async16(dst + (uint32_t)(ch >> 3) * kHalf +
+                                           (uint32_t)(rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)),
+                                       src + (in ? o + 8 * ch : 0), in);
+                        }
+                    cp_async_commit();
+                    if (kv && (j < ilo || j + kTaKeys > ihi)) {
+                        look |= 1u << (u & 7);
+                        mark = (mark & ~(15u << (4 * (u & 7)))) | ((uint32_t)(seg_no & 15) << (4 * (u & 7)));
+                    }
+                    if (u + 1 > told + kTaLag) {
+                        cp_async_wait<kTaLag>();
+                        signal(u + 1 - kTaLag);
+                    }
+                }
+            }
+            if (e.nt > 0) ++seg_no;
+        }
+        cp_async_wait<0>();
+        signal(u);
+        if (!ok) give_up();
+    } else {
+        // ---- products ----
+        uint32_t u = 0, np[2] = {0, 0};                  // ring tiles used, P's waited for
+        int seg_no = 0;
+        bool ok = true;
+        while (ok && next()) {
+            if (e.nt == 0) continue;
+            if (lane == 0) {
+                auto wait = [&](uint64_t* bar, uint32_t par) {
+                    if (ok && !ta_wait(bar, par, abort_flag)) ok = false;
+                    tc_fence_after();
+                };
+                auto scores = [&](int acc, uint32_t st) {
+#pragma unroll
+                    for (int kk = 0; kk < DP / 16; ++kk) {
+                        const uint32_t o = (uint32_t)(kk >> 2) * kHalf + 32u * (kk & 3);
+                        tc_mma_f16(tmem + 128u * acc, tc_sdesc_sw128(sQ + acc * kTile + o),
+                                   tc_sdesc_sw128(sRing + st * kTile + o), g.idesc_s, kk != 0);
+                    }
+                    tc_commit(sfull + acc);
+                };
+                wait(qfull, seg_no & 1);
+                wait(full + u % NS, (u / NS) & 1);
+                if (ok) {
+                    scores(0, u % NS);
+                    scores(1, u % NS);
+                    tc_commit(empty + u % NS);
+                }
+                for (int i = 0; i < e.nt && ok; ++i) {
+                    const uint32_t uv = u + 1, uk = u + 2;
+                    wait(full + uv % NS, (uv / NS) & 1);
+#pragma unroll
+                    for (int acc = 0; acc < 2; ++acc) {
+                        wait(pfull + acc, np[acc] & 1);
+                        ++np[acc];
+                        if (ok) {
+#pragma unroll
+                            for (int kk = 0; kk < kTaKeys / 16; ++kk)
+                                tc_mma_f16_ta(tmem + kColO + 128u * acc, tmem + 128u * acc + 8u * kk,
+                                              tc_sdesc_sw128_nmajor(sRing + (uv % NS) * kTile + 2048u * kk, kHalf),
+                                              g.idesc_o, (i | kk) != 0);
+                            if (acc == 1) tc_commit(empty + uv % NS);
+                            if (i + 1 == e.nt) tc_commit(ofull + acc);
+                        }
+                        if (i + 1 < e.nt) {
+                            if (acc == 0) wait(full + uk % NS, (uk / NS) & 1);
+                            if (ok) {
+                                scores(acc, uk % NS);
+                                if (acc == 1) tc_commit(empty + uk % NS);
+                            }
+                        }
+                    }
+                    u += 2;
+                }
+                if (!ok) give_up();
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+            ++seg_no;
+        }
+        if (lane == 0) {
+            // The products in flight end before the tensor memory is freed.
+            tc_commit(idle);
+            ta_wait(idle, 0, never);
+        }
+        __syncwarp();
+    }
+    } else {
+        // ---- softmax: a thread has row `row` of accumulator `acc` ----
+        const int acc = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + 128u * acc, tO = tmem + lanes + kColO + 128u * acc;
+        uint32_t ns = 0;                                 // S's waited for
+        int q_no = 0;                                    // pieces with keys
+        bool ok = true;
+        const bool neg = a.scale_log2 < 0.f, flat = a.scale_log2 == 0.f;
+        const float sc = flat ? 1.f : fabsf(a.scale_log2);
+        while (next()) {
+            const int64_t r0 = (int64_t)e.rt * kTaRows + acc * 128;      // of the sequence's rows
+            const int64_t n_rows = (int64_t)e.n * a.group;
+            if (e.nt > 0) {
+                // Queries of this accumulator.
+                for (int x = threadIdx.x & 127; x < 128 * CH; x += 128) {
+                    const int rr = x / CH, ch = x % CH;
+                    const int64_t r = r0 + rr, t = r / a.group;
+                    const bool in = r < n_rows && 8 * ch < D;
+                    const int64_t at = in ? (e.first + t) * a.q_stride + (int64_t)(e.hk * a.group + (int)(r - t * a.group)) * D + 8 * ch : 0;
+                    cp_async16(sQ + acc * kTile + (uint32_t)(ch >> 3) * kHalf +
+                                   (uint32_t)(rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)),
+                               static_cast<const T*>(a.q) + at, in);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qfull);
+                ++q_no;
+            }
+            // Keys that this row sees, and that all rows of the warp see.
+            int lo = 0, hi = 0;
+            const int64_t r = r0 + row;
+            if (r < n_rows) seen_range(a, e.len, e.n, (int)(r / a.group), lo, hi);
+            int wlo = r < n_rows ? lo : 0, whi = r < n_rows ? hi : INT32_MAX;
+            for (int x = 16; x; x >>= 1) {
+                wlo = max(wlo, __shfl_xor_sync(0xFFFFFFFFu, wlo, x));
+                whi = min(whi, __shfl_xor_sync(0xFFFFFFFFu, whi, x));
+            }
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < e.nt && ok; ++i) {
+                ok = __all_sync(0xFFFFFFFFu, ta_wait(sfull + acc, ns & 1, abort_flag));
+                ++ns;
+                if (!ok) break;
+                tc_fence_after();
+                // The row's 128 scores, 32 columns at a time: once for the
+                // maximum, then (the first half read again: registers) for
+                // the weights, which go where the scores were just taken from.
+                const int j = e.j0 + i * kTaKeys;
+                const int c0 = lo - j, c1 = hi - j;
+                const bool masked = j < wlo || j + kTaKeys > whi;
+                auto prepare = [&](float (&v)[32], int x) {
+                    if (neg || flat)
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) v[y] = neg ? -v[y] : 0.f * v[y];
+                    if (masked)
+#pragma unroll
+                        for (int y = 0; y < 32; ++y)
+                            if (32 * x + y < c0 || 32 * x + y >= c1) v[y] = -INFINITY;
+                };
+                auto largest = [&](const float (&v)[32]) {
+                    float m0 = v[0], m1 = v[1];
+#pragma unroll
+                    for (int y = 2; y < 32; y += 2) {
+                        m0 = fmaxf(m0, v[y]);
+                        m1 = fmaxf(m1, v[y + 1]);
+                    }
+                    return fmaxf(m0, m1);
+                };
+                float sa[32], sb[32], sd[32];
+                tc_ld32(tS, sa);
+                tc_wait_ld(sa);
+                tc_ld32(tS + 32u, sb);
+                prepare(sa, 0);
+                float top = largest(sa);
+                tc_wait_ld(sb);
+                tc_ld32(tS + 64u, sd);
+                prepare(sb, 1);
+                top = fmaxf(top, largest(sb));
+                tc_wait_ld(sd);
+                tc_ld32(tS + 96u, sb);
+                prepare(sd, 2);
+                top = fmaxf(top, largest(sd));
+                tc_wait_ld(sb);
+                prepare(sb, 3);
+                top = fmaxf(top, largest(sb)) * sc;
+                float f = 1.f;
+                if (i == 0) {
+                    m = top;
+                } else if (top > m + 8.f) {
+                    f = exp2f(m - top);
+                    m = top;
+                    l *= f;
+                }
+                if (__any_sync(0xFFFFFFFFu, f != 1.f)) {
+                    // S came after the last P V, so the sums are at rest.
+#pragma unroll 1
+                    for (int x = 0; x < DP / 32; ++x) {
+                        float o[32];
+                        uint32_t ow[32];
+                        tc_ld32(tO + 32u * x, o);
+                        tc_wait_ld(o);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) ow[y] = __float_as_uint(o[y] * f);
+                        tc_st32(tO + 32u * x, ow);
+                    }
+                }
+                const float mu = m == -INFINITY ? 0.f : m;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
+                auto weights = [&](const float (&v)[32], int x) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        float2 t = ffma2(make_float2(v[2 * y], v[2 * y + 1]), sc2, mu2);
+                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(t.x));
+                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(t.y));
+                        sum[y & 1] = fadd2(sum[y & 1], t);
+                        pw[y] = Elem<T>::pack(t.x, t.y);
+                    }
+                    tc_st16(tS + 16u * x, pw);
+                };
+                tc_ld32(tS, sa);
+                tc_wait_ld(sa);
+                prepare(sa, 0);
+                weights(sa, 0);
+                tc_ld32(tS + 32u, sa);
+                tc_wait_ld(sa);
+                prepare(sa, 1);
+                weights(sa, 1);
+                weights(sd, 2);
+                weights(sb, 3);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull + acc);
+            }
+            if (ok && e.nt > 0) {
+                ok = __all_sync(0xFFFFFFFFu, ta_wait(ofull + acc, (q_no - 1) & 1, abort_flag));
+                tc_fence_after();
+            }
+            // After a wait that gave up, the warp still meets the others at the
+            // barriers below and they end together.
+            if (!ok) give_up();
+            // The copying warps' marks on this piece reach here through the
+            // products' barriers; they are at most five pieces ahead.
+            const bool rows_apart = e.nt > 0 && odd[(q_no - 1) & 15] != 0;
+            float* slot = g.ws + (2 * (int64_t)blockIdx.x + e.slot) * ta_slot(DP);
+            if (e.pieces == 1) {
+                if (!rows_apart) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    const int64_t t = r / a.group;
+                    T* out = static_cast<T*>(a.out) + (e.first + t) * a.o_stride +
+                             (int64_t)(e.hk * a.group + (int)(r - t * a.group)) * D;
+#pragma unroll
+                    for (int x = 0; x < DP / 32; ++x) {
+                        float o[32];
+                        if (e.nt > 0) {
+                            tc_ld32(tO + 32u * x, o);
+                            tc_wait_ld(o);
+                        }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            float v[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) v[z] = e.nt > 0 ? o[8 * y + z] * inv : 0.f;
+                            if (r < n_rows && 32 * x + 8 * y < D) *reinterpret_cast<uint4*>(out + 32 * x + 8 * y) = pack8<T>(v);
+                        }
+                    }
+                }
+            } else {
+                // A piece: sums as [column / 4][row][4], so a warp's stores are
+                // 512 contiguous bytes.  The mark for a row-by-row unit is a
+                // weights' sum of -1.
+                const int rr = acc * 128 + row;
+#pragma unroll
+                for (int x = 0; x < DP / 32; ++x) {
+                    float o[32];
+                    if (e.nt > 0) {
+                        tc_ld32(tO + 32u * x, o);
+                        tc_wait_ld(o);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            *reinterpret_cast<float4*>(slot + ((8 * x + y) * kTaRows + rr) * 4) =
+                                make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                    }
+                }
+                slot[kTaRows * DP + rr] = m;
+                slot[kTaRows * DP + kTaRows + rr] = rows_apart ? -1.f : l;
+                __threadfence();
+                bar_softmax();
+                if (threadIdx.x == 0) *last_word = atom_add_acq_rel_gpu(g.cnt + e.c_lo, 1) == e.pieces - 1;
+                bar_softmax();
+            }
+            tc_fence_before();           // the sums were read: the next piece's products may come
+            bool apart = e.pieces == 1 && rows_apart;
+            if (e.pieces > 1 && *last_word) {
+                __threadfence();
+                if (threadIdx.x == 0) g.cnt[e.c_lo] = 0;
+                const int rr = acc * 128 + row;
+                float top = -INFINITY, sum = 0.f;
+                for (int p = 0; p < e.pieces; ++p) {
+                    const float* sp = g.ws + ta_piece(w, e, p) * ta_slot(DP) + kTaRows * DP + rr;
+                    top = fmaxf(top, __ldcg(sp));
+                    if (__ldcg(sp + kTaRows) == -1.f) apart = true;
+                }
+                const float mu = top == -INFINITY ? 0.f : top;
+                for (int p = 0; p < e.pieces; ++p) {
+                    const float* sp = g.ws + ta_piece(w, e, p) * ta_slot(DP) + kTaRows * DP + rr;
+                    sum += exp2f(__ldcg(sp) - mu) * __ldcg(sp + kTaRows);
+                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const int64_t t = r / a.group;
+                T* out = static_cast<T*>(a.out) + (e.first + t) * a.o_stride +
+                         (int64_t)(e.hk * a.group + (int)(r - t * a.group)) * D;
+#pragma unroll 1
+                for (int x = 0; x < DP / 32; ++x) {
+                    float4 o[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int p = 0; p < e.pieces; ++p) {
+                        const float* sp = g.ws + ta_piece(w, e, p) * ta_slot(DP);
+                        const float wt = exp2f(__ldcg(sp + kTaRows * DP + rr) - mu);
+                        if (wt == 0.f) continue;         // no keys: the slot's sums were not written
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(sp + ((8 * x + y) * kTaRows + rr) * 4));
+                            o[y].x += wt * v.x;
+                            o[y].y += wt * v.y;
+                            o[y].z += wt * v.z;
+                            o[y].w += wt * v.w;
+                        }
+                    }
+                    if (r < n_rows)
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            if (32 * x + 4 * y < D)
+                                *reinterpret_cast<uint2*>(out + 32 * x + 4 * y) =
+                                    make_uint2(Elem<T>::pack(o[y].x * inv, o[y].y * inv),
+                                               Elem<T>::pack(o[y].z * inv, o[y].w * inv));
+                }
+            }
+            bar_softmax();               // everyone has read this piece's mark and the word above
+            if (threadIdx.x == 0) {
+                if (e.nt > 0) odd[(q_no - 1) & 15] = 0;
+                *stop = *abort_flag;
+            }
+            bar_softmax();
+            if (*stop) break;
+            if (apart) {
+                for (int x = warp; x < kTaRows; x += 8) {
+                    const int64_t rx = (int64_t)e.rt * kTaRows + x;
+                    if (rx >= n_rows) break;
+                    const int t = (int)(rx / a.group);
+                    int l0, h0;
+                    seen_range(a, e.len, e.n, t, l0, h0);
+                    attend_row<T>(a, e.s, e.first + t, e.hk * a.group + (int)(rx - (int64_t)t * a.group), l0, h0);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace q4

@@ -8,6 +8,7 @@
 
 #include "../../include/q4gemv.h"
 #include "attn_split.cuh"
+#include "attn_tc.cuh"
 #include "ctx_view.h"
 #include "kv_append.cuh"
 #include "lin_chunk.cuh"
@@ -124,6 +125,8 @@ q4::RaggedArgs ragged(int64_t rows, int64_t n_seqs, const int32_t* start, const 
     return b;
 }
 
+// Rows of a sequence up to which attn_split_kernel takes it.
+constexpr int kSplitRowsMax = 64;
 // Up to this many new tokens of a sequence run token by token.
 constexpr int kLinRecurMax = 8;
 
@@ -146,6 +149,17 @@ cudaError_t split_setup() {
                                 q4::split_smem(DP));
 }
 
+template <typename T>
+cudaError_t tc_launch(const q4::TcAttnArgs& g, int sms, cudaStream_t st) {
+    return g.a.kv.head_dim <= 64
+               ? launch(q4::attn_tc_kernel<T, 64>, dim3((unsigned)sms), q4::kTaThreads, q4::ta_smem(64), st, g)
+               : launch(q4::attn_tc_kernel<T, 128>, dim3((unsigned)sms), q4::kTaThreads, q4::ta_smem(128), st, g);
+}
+template <typename T, int DP>
+cudaError_t tc_setup() {
+    return cudaFuncSetAttribute(q4::attn_tc_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, q4::ta_smem(DP));
+}
+
 template <typename T, int DK, int MT>
 cudaError_t chunk_setup() {
     return cudaFuncSetAttribute(q4::lin_chunk_kernel<T, DK, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -153,7 +167,8 @@ cudaError_t chunk_setup() {
 }
 template <typename T>
 cudaError_t setup_type() {
-    for (cudaError_t e : {split_setup<T, 64>(), split_setup<T, 128>(), split_setup<T, 256>(), chunk_setup<T, 64, 1>(),
+    for (cudaError_t e : {split_setup<T, 64>(), split_setup<T, 128>(), split_setup<T, 256>(), tc_setup<T, 64>(),
+                          tc_setup<T, 128>(), chunk_setup<T, 64, 1>(),
                           chunk_setup<T, 64, 2>(), chunk_setup<T, 128, 1>(), chunk_setup<T, 128, 2>(),
                           chunk_setup<T, 256, 1>()})
         if (e != cudaSuccess) return e;
@@ -182,6 +197,7 @@ void q4::mix_workspace(int sms, size_t* ws_bytes, size_t* cnt_bytes) {
         floats = std::max(floats, 2 * n * q4::split_slot(dp));
         ctas = std::max(ctas, n);
     }
+    floats = std::max(floats, 2 * (size_t)sms * q4::ta_slot(128));
     *ws_bytes = floats * sizeof(float);
     *cnt_bytes = ctas * sizeof(int);
 }
@@ -311,14 +327,32 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
     a.cap = (int)std::min<int64_t>(kv->table_cols * kv->page_size, INT32_MAX - 4096);
     a.err = cx.err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool f16 = kv->dtype == Q4GEMV_F16;
+    // Sequences with many rows (new tokens times query heads of a key head) go
+    // to the tensor-core kernel, those with few to the other; a batch that may
+    // hold both runs both.
+    const bool many = kv->head_dim <= 128 && max_new > kSplitRowsMax / a.group;
+    const bool few = !many || n_seqs > 1;
+    if (many) {
+        q4::TcAttnArgs g;
+        g.a = a;
+        g.ws = cx.attn_ws;
+        g.cnt = cx.attn_cnt;
+        g.min_rows = few ? kSplitRowsMax : 0;
+        g.min_cost = 768;
+        const int dp = kv->head_dim <= 64 ? 64 : 128;
+        g.idesc_s = q4::tc_idesc_16(128, q4::kTaKeys, !f16, false);
+        g.idesc_o = q4::tc_idesc_16(128, dp, !f16, true);
+        const int e = launch_status(h, f16 ? tc_launch<__half>(g, cx.sms, st) : tc_launch<__nv_bfloat16>(g, cx.sms, st), call);
+        if (e != Q4_OK || !few) return e;
+    }
     q4::SplitAttnArgs g;
     g.a = a;
     g.ws = cx.attn_ws;
     g.cnt = cx.attn_cnt;
-    g.max_rows = 0;
+    g.max_rows = many ? kSplitRowsMax : 0;
     g.min_blocks = 2;
-    return launch_status(h, kv->dtype == Q4GEMV_F16 ? split_launch<__half>(g, cx.sms, st)
-                                                    : split_launch<__nv_bfloat16>(g, cx.sms, st), call);
+    return launch_status(h, f16 ? split_launch<__half>(g, cx.sms, st) : split_launch<__nv_bfloat16>(g, cx.sms, st), call);
 }
 
 }  // extern "C"

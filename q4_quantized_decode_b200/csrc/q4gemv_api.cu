@@ -1655,6 +1655,11 @@ int q4gemv_sync_status(q4gemv_t h, q4gemv_stream_t stream) {
     Q4_CUDA(h, cudaMemcpy(&word, h->err, sizeof(int), cudaMemcpyDeviceToHost));
     if (word != 0) {
         Q4_CUDA(h, cudaMemset(h->err, 0, sizeof(int)));
+        if (word == q4::kDevTimeout) {   // arrival counts that a wait's end left behind
+            size_t ws_bytes = 0, cnt_bytes = 0;
+            q4::mix_workspace(h->sms, &ws_bytes, &cnt_bytes);
+            Q4_CUDA(h, cudaMemset(h->attn_cnt, 0, cnt_bytes));
+        }
         if (word == q4::kDevTimeout) return fail(h, Q4_ETIMEOUT, "device wait timed out");
         if (word == q4::kDevConcurrent) return fail(h, Q4_ECONCURRENT, "overlapping calls detected");
         if (word == q4::kDevIndex) return fail(h, Q4_EINDEX, "a page, place or state slot was out of range");
