@@ -308,19 +308,25 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+import torch as _torch  # noqa: E402  (after the library: a missing one is reported first)
+
+_raw_stream = _torch._C._cuda_getCurrentRawStream   # current_stream(device).cuda_stream, without the object
+
+
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.float16:
+    if t.dtype is _torch.float16:
         return F16
-    if t.dtype == torch.bfloat16:
+    if t.dtype is _torch.bfloat16:
         return BF16
     raise Q4Error(Q4_EINVAL, f"tensor of {t.dtype}: float16 or bfloat16 expected")
 
 
 def _heads(t, name: str, dtype, device, rows=None, heads=None, dim=None):
     """Row stride of t [rows][heads][dim], its heads and elements packed in a row."""
-    if t.dtype != dtype or t.device != device:
+    if t.dtype is not dtype or t.device != device:
         raise Q4Error(Q4_EINVAL, f"{name}: {t.dtype} on {t.device}, {dtype} on {device} expected")
+    if t.dim() != 3:
+        raise Q4Error(Q4_ESHAPE, f"{name}: shape {tuple(t.shape)}, [rows][heads][dim] expected")
     n, m, d = t.shape
     if (rows is not None and n != rows) or (heads is not None and m != heads) or (dim is not None and d != dim):
         raise Q4Error(Q4_ESHAPE, f"{name}: shape {tuple(t.shape)}, ({rows}, {heads}, {dim}) expected")
@@ -331,10 +337,9 @@ def _heads(t, name: str, dtype, device, rows=None, heads=None, dim=None):
 
 
 def _ints(t, name: str, device, n: int):
-    import torch
-    if t.dtype != torch.int32 or t.device != device:
+    if t.dtype is not _torch.int32 or t.device != device:
         raise Q4Error(Q4_EINVAL, f"{name}: {t.dtype} on {t.device}, int32 on {device} expected")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise Q4Error(Q4_ESHAPE, f"{name}: {n} contiguous entries expected")
     return t.data_ptr()
 
@@ -345,13 +350,12 @@ class PagedKV:
     will do) and the page table, int32 [sequences][pages of a sequence].  Keeps the tensors alive."""
 
     def __init__(self, k, v, table):
-        import torch
         dt = _dtype_code(k)
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
             raise Q4Error(Q4_ESHAPE, "k and v: one shape, type and layout [pages][page_size][heads][head_dim]")
         if k.stride(3) != 1 and k.shape[3] != 1:
             raise Q4Error(Q4_ESHAPE, "k and v: head_dim must be contiguous")
-        if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        if table.dtype != _torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
             raise Q4Error(Q4_ESHAPE, "table: int32 [sequences][pages of a sequence] expected")
         if not (k.device == v.device == table.device) or k.device.type != "cuda":
             raise Q4Error(Q4_EINVAL, "k, v and table: one CUDA device expected")
@@ -506,36 +510,32 @@ class Q4Gemv:
             raise Q4Error(Q4_EINVAL, f"tensors on {device}, the handle is on cuda:{self.device}")
 
     def _stream_of(self, stream) -> int:
-        import torch
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return _raw_stream(self.device)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
     def _new(self, shape, dtype, stream):
         """An output, from the pool of the stream that writes it."""
-        import torch
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
+            return _torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
+            stream = _torch.cuda.ExternalStream(int(stream), device=self.device)
+        with _torch.cuda.stream(stream):
+            return _torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
 
     def rope_freqs(self, rot: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0,
                    trained: float = 0.0, lo: float = 1.0, hi: float = 32.0):
         """float64 [rot/2] on the handle's device: radians per position of each pair."""
-        import torch
         st, f = q4gemv_rope_freqs(kind, rot, base, factor, trained, lo, hi)
         if st != Q4_OK:
             raise Q4Error(st, f"rope_freqs: {q4gemv_strerror(st)}")
-        return torch.tensor(f, dtype=torch.float64, device=f"cuda:{self.device}")
+        return _torch.tensor(f, dtype=_torch.float64, device=f"cuda:{self.device}")
 
     def kv_append(self, cache, start, length, k, v, q=None, q_out=None, freqs=None,
                   interleaved: bool = False, amp: float = 1.0, pos=None, stream=None):
         """Appends k, v [rows][heads][head_dim] to the cache, k rotated; returns q
         [rows][q_heads][head_dim] rotated (None without q).  freqs: float64 [rot/2] or None (no
         rotation); pos: int32 [rows] rotation positions, by default the places in the cache."""
-        import torch
         self._on_device(cache.device)
         c = cache.args
         n_seqs = length.shape[0]
@@ -555,7 +555,7 @@ class Q4Gemv:
             qp, qop = q.data_ptr(), q_out.data_ptr()
         rope = None
         if freqs is not None:
-            if freqs.dtype != torch.float64 or freqs.device != cache.device or not freqs.is_contiguous():
+            if freqs.dtype != _torch.float64 or freqs.device != cache.device or not freqs.is_contiguous():
                 raise Q4Error(Q4_EINVAL, "freqs: contiguous float64 on the cache's device expected")
             rope = q4gemv_rope(freqs.data_ptr(), 2 * freqs.numel(), int(interleaved), amp)
         self._check(_lib.q4gemv_kv_append(
@@ -592,7 +592,6 @@ class Q4Gemv:
         log_decay float32 [rows][v_heads] (an expanded row: fixed decays), state float32
         [slots][v_heads][k_dim][v_dim] (updated in place unless state_out is given; None: from
         zeros into state_out).  Returns (out, state_out)."""
-        import torch
         if state_out is None:
             state_out = state
         if state_out is None:
@@ -609,12 +608,12 @@ class Q4Gemv:
         if out is None:
             out = self._new((rows, hv, dv), q.dtype, stream)
         os_ = _heads(out, "out", q.dtype, dev, rows, hv, dv)
-        if log_decay.dtype != torch.float32 or log_decay.device != dev or log_decay.shape != (rows, hv) or \
+        if log_decay.dtype != _torch.float32 or log_decay.device != dev or log_decay.shape != (rows, hv) or \
                 (hv > 1 and log_decay.stride(1) != 1):
             raise Q4Error(Q4_ESHAPE, f"log_decay: float32 [{rows}][{hv}] on {dev} expected")
         n_slots = state_out.shape[0]
         for t in (state, state_out):
-            if t is not None and (t.dtype != torch.float32 or t.device != dev or not t.is_contiguous() or
+            if t is not None and (t.dtype != _torch.float32 or t.device != dev or not t.is_contiguous() or
                                   t.shape != (n_slots, hv, dk, dv)):
                 raise Q4Error(Q4_ESHAPE, f"state: contiguous float32 [{n_slots}][{hv}][{dk}][{dv}] on {dev} expected")
         a = q4gemv_linattn_args(

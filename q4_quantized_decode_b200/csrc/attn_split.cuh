@@ -75,17 +75,6 @@ __device__ __forceinline__ SeqWork seq_work(const SplitAttnArgs& g, int s) {
     return w;
 }
 
-// Whether any of eight 16-bit values is an infinity or NaN.
-template <typename T>
-__device__ __forceinline__ bool any_nonfinite(uint4 v) {
-    constexpr uint32_t e = Elem<T>::kExpMask;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (w[i] & e) == e || (w[i] & (e << 16)) == (e << 16);
-    return bad;
-}
-
 template <typename T, int DP>
 __global__ void __launch_bounds__(kSplitThreads, split_ctas_per_sm(DP)) attn_split_kernel(const SplitAttnArgs g) {
     constexpr int CH = DP / 8;                            // 16-byte chunks of a padded head

@@ -12,10 +12,12 @@
 //              than 2^8 (until then P may pass 1 and stays far from overflow);
 //   warp 8     one thread issues the products: S of one accumulator runs while
 //              the other one's softmax does;
-//   warps 9-11 the pages' rows into a ring of 128-key tiles (asynchronous
-//              16-byte copies, because pages end anywhere in a tile; keys that
-//              no row sees are zeros), in the 128-byte swizzle that the
-//              products read: K as rows of K, V as an N-major operand.
+//   warps 9-10 the pages' rows into a ring of 128-key tiles, in the 128-byte
+//              swizzle that the products read (K as rows of K, V as an N-major
+//              operand): tiles that every row sees whole by tensor map, where
+//              pages of 8, 16, .. tokens allow it, the others by asynchronous
+//              16-byte copies, because pages may end anywhere in a tile and
+//              keys that no row sees have to be zeros.
 // Two products of 128 x 128 x head_dim for each accumulator and tile, 16384
 // powers of two: the tensor pipe and the exponential unit need about the same
 // time, 2048 cycles for a CTA's tile at head size 128, and bound this together.
@@ -32,6 +34,8 @@
 // a unit with such a value, or with a bad page, is taken row by row at the end.
 #pragma once
 
+#include <cuda.h>
+
 #include "attn_rows.cuh"
 #include "mma_common.cuh"
 #include "tc_common.cuh"
@@ -40,7 +44,7 @@ namespace q4 {
 
 constexpr int kTaRows = 256;                 // rows of a unit
 constexpr int kTaKeys = 128;                 // keys of a tile
-constexpr int kTaLoaders = 3;
+constexpr int kTaLoaders = 2;
 constexpr int kTaThreads = 32 * (8 + 1 + kTaLoaders);
 constexpr int kTaLag = 2;                    // copies in flight behind the newest
 constexpr int kTaOver = 128;                 // a unit's fixed cost in keys: its start and end
@@ -60,6 +64,8 @@ struct TcAttnArgs {
     int min_rows;        // sequences of at most this many rows are another kernel's
     int min_cost;        // keys of a run, at least
     uint32_t idesc_s, idesc_o;
+    int box;             // tokens of a tensor-map box (8..128, page_size or 128), 0: no maps
+    CUtensorMap kmap, vmap;   // [page][head][token][element], boxes of 64 elements x `box` tokens
 };
 
 // The units of a sequence: `tiles` row tiles, of cost c0 + c1 rt each.
@@ -267,6 +273,16 @@ __device__ __forceinline__ int64_t ta_piece(const TaWalk& w, const TaSeg& e, int
     return 2 * c + (w.k == 0 && ta_cut(w.total, w.runs, c) < e.ub ? 1 : 0);
 }
 
+// A box of a 4-dimensional tensor map into shared memory; its bytes count on
+// `bar`.  x is a multiple of 64 elements.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+                 : "memory");
+}
+
 // A wait that gives up when another role has, or after about 20 seconds (the
 // longest that a role keeps others waiting in earnest is a unit taken row by
 // row, milliseconds for ordinary contexts).
@@ -282,7 +298,7 @@ __device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity, volatile
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const TcAttnArgs g) {
+__global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnArgs g) {
     constexpr int NS = ta_slots(DP);
     constexpr int CH = DP / 8;
     constexpr uint32_t kHalf = kTaKeys * 128;            // one 64-element part of a 128-row tile
@@ -364,10 +380,15 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const TcAttnArgs
         const int lw = warp - 9;
         uint32_t u = 0;                                  // tiles begun
         uint32_t told = 0;                               // tiles whose arrival was signalled
-        int64_t off[4];
         uint32_t look = 0, mark = 0;                     // of the tiles in flight: V tiles to look over, their pieces
         int seg_no = 0;
         bool ok = true;
+        // This warp's 64 keys of a tile, two a lane; copies of a tile are
+        // CH per 32 keys, `ch` of every 32 / CH-th row.
+        constexpr int RPI = 32 / CH;                     // rows of a copy instruction
+        const int ch = lane % CH;
+        const uint32_t col = (uint32_t)(ch >> 3) * kHalf;
+        auto place = [&](int rr) { return col + (uint32_t)(rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)); };
         auto signal = [&](uint32_t upto) {
             for (; told < upto; ++told) {
                 const uint32_t st = told % NS;
@@ -375,18 +396,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const TcAttnArgs
                     // this thread's own chunks of a V tile
                     bool bad = false;
                     const uint32_t vt = sRing + st * kTile;
-#pragma unroll
-                    for (int gq = 0; gq < 4; ++gq)
-                        for (int x = lw; x < 32 * CH / 32; x += kTaLoaders) {
-                            const int ci = x * 32 + lane, row = 32 * gq + ci / CH, ch = ci % CH;
-                            const uint4 v = lds128(vt + (uint32_t)(ch >> 3) * kHalf +
-                                                   (uint32_t)(row * 128 + (((ch & 7) ^ (row & 7)) << 4)));
-                            constexpr uint32_t ex = Elem<T>::kExpMask;
-                            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                bad |= (vw[y] & ex) == ex || (vw[y] & (ex << 16)) == (ex << 16);
-                        }
+#pragma unroll 8
+                    for (int x = 0; x < 64 / RPI; ++x)
+                        bad |= any_nonfinite<T>(lds128(vt + place(64 * lw + x * RPI + lane / CH)));
                     if (bad) odd[(mark >> (4 * (told & 7))) & 15] = 1;
                     look &= ~(1u << (told & 7));
                 }
@@ -403,20 +415,53 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const TcAttnArgs
             int ilo, ihi, x0;
             seen_range(a, e.len, e.n, t1, ilo, x0);
             seen_range(a, e.len, e.n, t0, x0, ihi);
-            for (int i = 0; i < e.nt && ok; ++i) {
-                const int j = e.j0 + i * kTaKeys;
-                bool page_bad = false;
+            const int j_first = e.j0, nt = e.nt, tlo = e.tlo, thi = e.thi, seq = e.s;
+            const int hk = e.hk;
+            // A tile that all rows see whole comes by tensor map, a page (or
+            // its part) a box; the others by 16-byte copies, which leave keys
+            // that no row sees zero.
+            auto by_map = [&](int j) { return g.box && j >= ilo && j + kTaKeys <= ihi; };
+            // Page of box lane / parts of the tile at j, or keys lane, lane + 32
+            // of this warp's.
+            const int parts = DP / 64, boxes = g.box ? kTaKeys / g.box : 0;
+            int pg = -1;
+            int64_t off[2] = {-1, -1};
+            bool page_bad = false;
+            auto lookup = [&](int j) {
+                if (by_map(j)) {
+                    pg = 0;
+                    if (lane < boxes * parts) {
+                        int page, row;
+                        split_page(a.kv, j + (lane / parts) * g.box, page, row);
+                        pg = a.kv.table[(int64_t)seq * a.kv.table_stride + page];      // inside the columns: j < cap
+                        if ((unsigned)pg >= (unsigned)a.kv.n_pages) {
+                            set_device_error(a.err, kDevIndex);
+                            page_bad = true;
+                            pg = 0;
+                        }
+                    }
+                } else {
 #pragma unroll
-                for (int gq = 0; gq < 4; ++gq) {
-                    const int key = j + 32 * gq + lane;
-                    off[gq] = -1;
-                    if (key >= e.tlo && key < e.thi) {
-                        off[gq] = token_offset(a.kv, e.s, key, a.err);
-                        if (off[gq] < 0) page_bad = true;
-                        else off[gq] += ho;
+                    for (int y = 0; y < 2; ++y) {
+                        const int key = j + 64 * lw + 32 * y + lane;
+                        off[y] = -1;
+                        if (key >= tlo && key < thi) {
+                            off[y] = token_offset(a.kv, seq, key, a.err);
+                            if (off[y] < 0) page_bad = true;
+                            else off[y] += ho;
+                        }
                     }
                 }
+            };
+            if (nt > 0) lookup(j_first);
+            for (int i = 0; i < nt && ok; ++i) {
+                const int j = j_first + i * kTaKeys;
+                const bool mapped = by_map(j);
+                const int pg_now = pg;
+                const int64_t off0 = off[0], off1 = off[1];
                 if (page_bad) odd[seg_no & 15] = 1;
+                page_bad = false;
+                if (i + 1 < nt) lookup(j + kTaKeys);     // the next tile's pages, on their way meanwhile
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++u) {
                     const uint32_t st = u % NS;
@@ -429,18 +474,37 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const TcAttnArgs
                             if (!ok) break;
                         }
                     }
-                    const T* src = static_cast<const T*>(kv ? a.kv.v : a.kv.k);
                     const uint32_t dst = sRing + st * kTile;
+                    if (mapped) {
+                        if (told < u) {
+                            cp_async_wait<0>();
+                            signal(u);
+                        }
+                        told = u + 1;
+                        if (lane == 0) {
+                            if (lw == 0) mbar_arrive_expect_tx(full + st, kTile);
+                            else mbar_arrive(full + st);
+                        }
+                        __syncwarp();
+                        if (lw == 0 && lane < boxes * parts) {
+                            const int box = lane / parts, part = lane - box * parts;
+                            int page, row;
+                            split_page(a.kv, j + box * g.box, page, row);
+                            tma_load_4d(dst + (uint32_t)part * kHalf + (uint32_t)(box * g.box) * 128u,
+                                        kv ? &g.vmap : &g.kmap, 64 * part, row, hk, pg_now, full + st);
+                        }
+                        continue;
+                    }
+                    const T* src = static_cast<const T*>(kv ? a.kv.v : a.kv.k) + 8 * ch;
+                    const bool chin = 8 * ch < D;
 #pragma unroll
-                    for (int gq = 0; gq < 4; ++gq)
-                        for (int x = lw; x < CH; x += kTaLoaders) {
-                            const int ci = x * 32 + lane, row = ci / CH, ch = ci % CH;
-                            const int64_t o = __shfl_sync(0xFFFFFFFFu, off[gq], row);
-                            const bool in = o >= 0 && 8 * ch < D;
-                            const int rr = 32 * gq + row;
-                            cp_async16(dst + (uint32_t)(ch >> 3) * kHalf +
-                                           (uint32_t)(rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)),
-                                       src + (in ? o + 8 * ch : 0), in);
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int x = 0; x < CH; ++x) {
+                            const int row = x * RPI + lane / CH;           // of 32
+                            const int64_t o = __shfl_sync(0xFFFFFFFFu, y ? off1 : off0, row);
+                            const bool in = o >= 0 && chin;
+                            cp_async16(dst + place(64 * lw + 32 * y + row), in ? src + o : static_cast<const T*>(a.kv.k), in);
                         }
                     cp_async_commit();
                     if (kv && (j < ilo || j + kTaKeys > ihi)) {
@@ -453,7 +517,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const TcAttnArgs
                     }
                 }
             }
-            if (e.nt > 0) ++seg_no;
+            if (nt > 0) ++seg_no;
         }
         cp_async_wait<0>();
         signal(u);

@@ -149,6 +149,33 @@ cudaError_t split_setup() {
                                 q4::split_smem(DP));
 }
 
+// Tensor map of one half of a paged cache for boxes of 64 elements x `box`
+// tokens in the 128-byte swizzle; false where the driver refuses it.
+bool page_map(CUtensorMap* map, void* base, const q4gemv_kv& c, int box) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.n_heads,
+                                (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, (cuuint64_t)c.head_stride * 2,
+                                   (cuuint64_t)c.page_stride * 2};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+    return encode(map, c.dtype == Q4GEMV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  base, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T>
 cudaError_t tc_launch(const q4::TcAttnArgs& g, int sms, cudaStream_t st) {
     return g.a.kv.head_dim <= 64
@@ -341,6 +368,10 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
         g.min_rows = few ? kSplitRowsMax : 0;
         g.min_cost = 768;
         const int dp = kv->head_dim <= 64 ? 64 : 128;
+        // Boxes of a page each (of 128 tokens in larger pages), where pages of
+        // a power of two from 8 on divide a tile or are divided by it.
+        g.box = a.kv.page_shift >= 3 ? std::min((int)kv->page_size, q4::kTaKeys) : 0;
+        if (g.box && !(page_map(&g.kmap, kv->k, *kv, g.box) && page_map(&g.vmap, kv->v, *kv, g.box))) g.box = 0;
         g.idesc_s = q4::tc_idesc_16(128, q4::kTaKeys, !f16, false);
         g.idesc_o = q4::tc_idesc_16(128, dp, !f16, true);
         const int e = launch_status(h, f16 ? tc_launch<__half>(g, cx.sms, st) : tc_launch<__nv_bfloat16>(g, cx.sms, st), call);

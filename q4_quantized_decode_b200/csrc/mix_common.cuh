@@ -57,6 +57,17 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       Elem<T>::pack(f[6], f[7]));
 }
 
+// Whether any of eight 16-bit values is an infinity or NaN.
+template <typename T>
+__device__ __forceinline__ bool any_nonfinite(uint4 v) {
+    constexpr uint32_t e = Elem<T>::kExpMask;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= (w[i] & e) == e || (w[i] & (e << 16)) == (e << 16);
+    return bad;
+}
+
 // The new tokens of a batch of sequences: sequence s holds the rows
 // [start[s], start[s + 1]).  Entries come from device memory and are not
 // trusted: rows outside [0, rows) belong to no sequence.
