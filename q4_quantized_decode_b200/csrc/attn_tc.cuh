@@ -45,8 +45,9 @@ namespace q4 {
 constexpr int kTaRows = 256;                 // rows of a unit
 constexpr int kTaKeys = 128;                 // keys of a tile
 constexpr int kTaLoaders = 2;
-constexpr int kTaThreads = 32 * (8 + 1 + kTaLoaders);
+constexpr int kTaThreads = 32 * 12;
 constexpr int kTaLag = 2;                    // copies in flight behind the newest
+constexpr int kTaSegs = 4;                   // parts told ahead
 constexpr int kTaOver = 128;                 // a unit's fixed cost in keys: its start and end
 
 // Ring slots (a K or a V tile each) beside the queries.
@@ -62,7 +63,6 @@ struct TcAttnArgs {
     float* ws;           // [2 * gridDim.x] slots
     int* cnt;            // [gridDim.x] arrivals, zero between calls
     int min_rows;        // sequences of at most this many rows are another kernel's
-    int min_cost;        // keys of a run, at least
     uint32_t idesc_s, idesc_o;
     int box;             // tokens of a tensor-map box (8..128, page_size or 128), 0: no maps
     CUtensorMap kmap, vmap;   // [page][head][token][element], boxes of 64 elements x `box` tokens
@@ -94,29 +94,33 @@ __device__ __forceinline__ TaSeq ta_seq(const TcAttnArgs& g, int s) {
     return q;
 }
 
-// A CTA's part of one unit.
+// A CTA's part of one unit, as the other warps get it.
 struct TaSeg {
-    int s, rt, hk;
-    int64_t first;
-    int n, len;
-    int j0;              // first key of the piece, a multiple of 128 over the pages
-    int nt;              // its 128-key tiles
+    int more;            // 0: no further part, the rest is not set
+    int s, hk, len, n;
+    int n_rows;          // rows of the unit
+    int t0, g0;          // token and query head (of the key head's) of its first row
+    int64_t first;       // the sequence's first row in the batch
+    int j0, nt;          // first key of the part (a multiple of 128), its 128-key tiles
     int tlo, thi;        // keys that any row of the unit sees
-    int pieces;          // pieces of the unit
-    int64_t c_lo;        // CTA of the first piece
-    int64_t ub;          // the unit's place on the cost line
-    int slot;            // 0: this CTA's first workspace slot, 1: its second
+    int pieces, c_lo;    // pieces of the unit, the CTA of the first
+    int slot, slot0;     // workspace slots of this piece and of the first
 };
 
-// Walks over a CTA's units; every warp does it for itself.
+__device__ __forceinline__ int64_t div_floor(int64_t a, int b) {      // a >= 0, b > 0
+    return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// Walks over a CTA's units (one warp, all lanes alike).
 struct TaWalk {
-    int64_t total, runs, b, b1, b0, seq_base;
-    int s, k;            // k > 0: few units, k CTAs for each
-    TaSeq q;
+    double ratio;        // cost of a run
+    int64_t total, b0, b1, b, seq_base;
+    int runs, s, k;      // k > 0: few units, k CTAs for each
     bool done;
-};
+    TaSeq q;
 
-__device__ __forceinline__ int64_t ta_cut(int64_t total, int64_t runs, int64_t c) { return c * total / runs; }
+    __device__ __forceinline__ int64_t cut(int c) const { return c >= runs ? total : (int64_t)((double)c * ratio); }
+};
 
 // The sequence whose units (by count, or by cost) hold place x.
 __device__ __forceinline__ void ta_find(const TcAttnArgs& g, int64_t x, bool by_units, int& s, int64_t& base) {
@@ -145,6 +149,66 @@ __device__ __forceinline__ void ta_find(const TcAttnArgs& g, int64_t x, bool by_
     }
 }
 
+// Place x of sequence q's cost (from its beginning): row tile, key head, place
+// within the unit.
+__device__ __forceinline__ void ta_unit(const TaSeq& q, int nh, int64_t x, int& rt, int& hk, int& in) {
+    const int64_t xh = div_floor(x, nh);
+    int64_t r;
+    if (q.c1 == 0) {
+        r = div_floor(xh, max(1, q.c0));
+    } else {
+        const float c1 = (float)q.c1, m = (float)q.c0 - 0.5f * c1;
+        r = (int64_t)((sqrtf(m * m + 2.f * c1 * (float)xh) - m) / c1);
+    }
+    r = max((int64_t)0, min(r, (int64_t)q.tiles - 1));
+    while (r > 0 && q.before(r) > xh) --r;
+    while (r + 1 < q.tiles && q.before(r + 1) <= xh) ++r;
+    const int cu = q.c0 + q.c1 * (int)r;
+    const int64_t rest = x - q.before(r) * nh;
+    rt = (int)r;
+    hk = (int)div_floor(rest, max(1, cu));
+    in = (int)(rest - (int64_t)hk * cu);
+}
+
+// Keys of row tile rt (the first row starts lowest, the last ends highest):
+// the first 128-key tile's first key, the tiles.
+__device__ __forceinline__ int ta_tiles(const TcAttnArgs& g, const TaSeq& q, int rt, int& tlo, int& thi, int& base) {
+    const int t0 = (int)div_floor((int64_t)rt * kTaRows, g.a.group);
+    const int t1 = min(q.n - 1, (int)div_floor((int64_t)(rt + 1) * kTaRows - 1, g.a.group));
+    int lo1, hi0;
+    seen_range(g.a, q.len, q.n, t0, tlo, hi0);
+    seen_range(g.a, q.len, q.n, t1, lo1, thi);
+    base = tlo / kTaKeys * kTaKeys;
+    return thi > tlo ? (thi - base + kTaKeys - 1) / kTaKeys : 0;
+}
+
+// Where a cut at place `in` of a unit with T tiles and cost cu falls: before
+// tile T * in / cu, or at the unit's begin (0) or end (T) where that leaves a
+// piece of under kTaPiece tiles: its way through the workspace costs more than
+// an uneven run.
+constexpr int kTaPiece = 6;
+__device__ __forceinline__ int ta_snap(int T, int in, int cu) {
+    const int i = (int)div_floor((int64_t)T * in, max(1, cu));
+    if (2 * i <= T) return i < kTaPiece ? 0 : T - i < kTaPiece ? T : i;
+    return T - i < kTaPiece ? T : i < kTaPiece ? 0 : i;
+}
+
+// Moves a cut to where ta_snap puts it; sets the walk's sequence to the one
+// that holds it.
+__device__ __forceinline__ int64_t ta_snapped(const TcAttnArgs& g, TaWalk& w, int c) {
+    if (c == 0) return 0;
+    if (c >= w.runs) return w.total;
+    const int64_t x = w.cut(c);
+    int s, rt, hk, in, lo, hi, base;
+    int64_t sb;
+    ta_find(g, x, false, s, sb);
+    const TaSeq q = ta_seq(g, s);
+    ta_unit(q, g.a.kv.n_heads, x - sb, rt, hk, in);
+    const int T = ta_tiles(g, q, rt, lo, hi, base), cu = q.c0 + q.c1 * rt;
+    const int i = ta_snap(T, in, cu);
+    return i == 0 ? x - in : i >= T ? x - in + cu : x;
+}
+
 __device__ __forceinline__ TaWalk ta_start(const TcAttnArgs& g) {
     TaWalk w;
     const int lane = threadIdx.x & 31, nh = g.a.kv.n_heads, n_seqs = g.a.batch.n_seqs;
@@ -163,11 +227,11 @@ __device__ __forceinline__ TaWalk ta_start(const TcAttnArgs& g) {
     w.k = 0;
     w.b0 = w.b = w.b1 = 0;
     if (w.done) return w;
-    const int64_t c = blockIdx.x;
+    const int c = blockIdx.x;
     if (2 * units <= (int64_t)gridDim.x) {
-        w.k = (int)(gridDim.x / units);
+        w.k = (int)(gridDim.x / (unsigned)units);
         w.runs = 0;
-        const int64_t u = c / w.k;
+        const int u = c / w.k;
         w.done = u >= units;
         if (w.done) return w;
         ta_find(g, u, true, w.s, w.seq_base);
@@ -175,102 +239,88 @@ __device__ __forceinline__ TaWalk ta_start(const TcAttnArgs& g) {
         w.b = u - w.seq_base;                 // the unit within the sequence
         return w;
     }
-    w.runs = min((int64_t)gridDim.x, max((int64_t)1, cost / g.min_cost));
-    w.done = c >= w.runs;
+    w.runs = (int)gridDim.x;
+    w.ratio = (double)cost / (double)w.runs;
+    w.b0 = w.b = ta_snapped(g, w, c);
+    w.b1 = ta_snapped(g, w, c + 1);
+    w.done = w.b >= w.b1;
     if (w.done) return w;
-    w.b0 = w.b = ta_cut(cost, w.runs, c);
-    w.b1 = ta_cut(cost, w.runs, c + 1);
     ta_find(g, w.b, false, w.s, w.seq_base);
     w.q = ta_seq(g, w.s);
     return w;
 }
 
-// The next part of this CTA's run; false at its end.
-__device__ __forceinline__ bool ta_next(const TcAttnArgs& g, TaWalk& w, TaSeg& e) {
-    if (w.done) return false;
+// The next part of this CTA's run; e.more = 0 at its end.
+__device__ __forceinline__ void ta_next(const TcAttnArgs& g, TaWalk& w, TaSeg& e) {
+    e.more = 0;
     const int nh = g.a.kv.n_heads;
-    int64_t v0 = 0, v1 = 1, cu = 1;           // the piece within the unit's cost
+    int rt, hk, in = 0, base, i0, i1;
+    if (w.done) return;
     if (w.k) {
-        e.rt = (int)(w.b / nh);
-        e.hk = (int)(w.b - (int64_t)e.rt * nh);
         w.done = true;
-    } else {
-        if (w.b >= w.b1) return false;
-        while (w.b >= w.seq_base + w.q.before(w.q.tiles) * nh && w.s + 1 < g.a.batch.n_seqs) {
-            w.seq_base += w.q.before(w.q.tiles) * nh;
-            w.q = ta_seq(g, ++w.s);
-        }
-        // The row tile whose units hold the place: before(rt) <= x / nh.
-        const int64_t x = w.b - w.seq_base, xh = x / nh;
-        int64_t rt;
-        if (w.q.c1 == 0) {
-            rt = xh / max(1, w.q.c0);
-        } else {
-            const double c1 = w.q.c1, m = w.q.c0 - 0.5 * c1;
-            rt = (int64_t)((sqrt(m * m + 2.0 * c1 * (double)xh) - m) / c1);
-        }
-        rt = max((int64_t)0, min(rt, (int64_t)w.q.tiles - 1));
-        while (rt > 0 && w.q.before(rt) > xh) --rt;
-        while (rt + 1 < w.q.tiles && w.q.before(rt + 1) <= xh) ++rt;
-        cu = w.q.c0 + (int64_t)w.q.c1 * rt;
-        const int64_t in = x - w.q.before(rt) * nh;
-        e.rt = (int)rt;
-        e.hk = (int)(in / cu);
-        v0 = in - e.hk * cu;
-        e.ub = w.b - v0;
-        v1 = min(cu, v0 + (w.b1 - w.b));
-        e.slot = w.b == w.b0 ? 0 : 1;
-        w.b += v1 - v0;
-    }
-    e.s = w.s;
-    e.first = w.q.first;
-    e.n = w.q.n;
-    e.len = w.q.len;
-    // Keys of the unit: the first row starts lowest, the last ends highest.
-    const int t0 = (int)((int64_t)e.rt * kTaRows / g.a.group);
-    const int t1 = min(e.n - 1, (int)(((int64_t)(e.rt + 1) * kTaRows - 1) / g.a.group));
-    int lo1, hi0;
-    seen_range(g.a, e.len, e.n, t0, e.tlo, hi0);
-    seen_range(g.a, e.len, e.n, t1, lo1, e.thi);
-    const int base = e.tlo / kTaKeys * kTaKeys;
-    const int T = e.thi > e.tlo ? (e.thi - base + kTaKeys - 1) / kTaKeys : 0;
-    if (w.k) {
+        rt = (int)div_floor(w.b, nh);
+        hk = (int)(w.b - (int64_t)rt * nh);
+        const int T = ta_tiles(g, w.q, rt, e.tlo, e.thi, base);
         // As many pieces as leave a piece about as many tiles as there are
         // pieces to join.
         int k = 1;
         while (k < w.k && (k + 1) * (k + 1) <= T) ++k;
         const int p = (int)(blockIdx.x % (unsigned)w.k);
-        if (p >= k) return false;
-        v0 = p;
-        v1 = p + 1;
-        cu = k;
-        e.c_lo = (int64_t)blockIdx.x - p;
+        if (p >= k) return;
+        i0 = (int)((int64_t)T * p / k);
+        i1 = (int)((int64_t)T * (p + 1) / k);
+        e.c_lo = (int)blockIdx.x - p;
         e.pieces = k;
-        e.slot = 0;
-        e.ub = 0;
-    } else if (v0 == 0 && v1 == cu) {
-        e.pieces = 1;
-        e.c_lo = blockIdx.x;
+        e.slot = 2 * (int)blockIdx.x;
+        e.slot0 = 2 * e.c_lo;
     } else {
-        auto cta_of = [&](int64_t x) {
-            int64_t c = x * w.runs / w.total;
-            while (c + 1 < w.runs && ta_cut(w.total, w.runs, c + 1) <= x) ++c;
-            while (c > 0 && ta_cut(w.total, w.runs, c) > x) --c;
-            return c;
-        };
-        e.c_lo = cta_of(e.ub);
-        e.pieces = (int)(cta_of(e.ub + cu - 1) - e.c_lo) + 1;
+        if (w.b >= w.b1) {
+            w.done = true;
+            return;
+        }
+        while (w.b >= w.seq_base + w.q.before(w.q.tiles) * nh && w.s + 1 < g.a.batch.n_seqs) {
+            w.seq_base += w.q.before(w.q.tiles) * nh;
+            w.q = ta_seq(g, ++w.s);
+        }
+        ta_unit(w.q, nh, w.b - w.seq_base, rt, hk, in);
+        const int cu = w.q.c0 + w.q.c1 * rt;
+        const int64_t ub = w.b - in, ue = ub + cu;
+        const int64_t stop = w.b1 < ue ? w.b1 : ue;
+        const int T = ta_tiles(g, w.q, rt, e.tlo, e.thi, base);
+        i0 = in == 0 ? 0 : (int)div_floor((int64_t)T * in, cu);
+        i1 = stop == ue ? T : (int)div_floor((int64_t)T * (stop - ub), cu);
+        // The runs that begin inside the unit are consecutive; the run before
+        // the first of them has the unit's first piece.
+        int c = (int)((double)ub / w.ratio);
+        c = max(0, min(c, w.runs - 1));
+        while (c > 0 && w.cut(c) > ub) --c;
+        while (c + 1 < w.runs && w.cut(c + 1) <= ub) ++c;
+        ++c;
+        int inside = 0, c_first = 0;
+        for (; c < w.runs && w.cut(c) < ue; ++c) {
+            const int i = ta_snap(T, (int)(w.cut(c) - ub), cu);
+            if (i > 0 && i < T) {
+                if (inside++ == 0) c_first = c;
+            }
+        }
+        e.pieces = inside + 1;
+        e.c_lo = inside ? c_first - 1 : (int)blockIdx.x;
+        e.slot = 2 * (int)blockIdx.x + (w.b == w.b0 ? 0 : 1);
+        e.slot0 = e.slot;
+        if (inside) e.slot0 = 2 * e.c_lo + (ta_snapped(g, w, e.c_lo) < ub ? 1 : 0);
+        w.b = stop;
     }
-    const int i0 = (int)(T * v0 / cu), i1 = (int)(T * v1 / cu);
+    e.more = 1;
+    e.s = w.s;
+    e.hk = hk;
+    e.len = w.q.len;
+    e.n = w.q.n;
+    e.first = w.q.first;
+    e.n_rows = (int)min((int64_t)kTaRows, (int64_t)w.q.n * g.a.group - (int64_t)rt * kTaRows);
+    e.t0 = (int)div_floor((int64_t)rt * kTaRows, g.a.group);
+    e.g0 = (int)((int64_t)rt * kTaRows - (int64_t)e.t0 * g.a.group);
     e.j0 = base + i0 * kTaKeys;
     e.nt = i1 - i0;
-    return true;
-}
-
-// Workspace slot of piece p of a unit.
-__device__ __forceinline__ int64_t ta_piece(const TaWalk& w, const TaSeg& e, int p) {
-    const int64_t c = e.c_lo + p;
-    return 2 * c + (w.k == 0 && ta_cut(w.total, w.runs, c) < e.ub ? 1 : 0);
 }
 
 // A box of a 4-dimensional tensor map into shared memory; its bytes count on
@@ -296,6 +346,16 @@ __device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity, volatile
 }
 
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The same; whether `ok` holds for all of them.
+__device__ __forceinline__ bool all_softmax(bool ok) {
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.cta.red.and.pred q, 1, 256, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all) : "r"((uint32_t)ok) : "memory");
+    return all != 0;
+}
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnArgs g) {
@@ -313,14 +373,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
     uint64_t* qfull = empty + NS;                        // queries in place
     uint64_t* sfull = qfull + 1;                         // [2] S computed
     uint64_t* pfull = sfull + 2;                         // [2] P written
-    uint64_t* ofull = pfull + 2;                         // [2] the piece's sums complete
-    uint64_t* idle = ofull + 2;                          // every product done
+    uint64_t* phalf = pfull + 2;                         // [2] the first 64 keys of P written
+    uint64_t* ofull = phalf + 2;                         // [2] the piece's sums complete
+    uint64_t* pfull_seg = ofull + 2;                     // [kTaSegs] a part is told
+    uint64_t* pempty_seg = pfull_seg + kTaSegs;          // [kTaSegs] every working warp is done with it
+    uint64_t* idle = pempty_seg + kTaSegs;               // every product done
     uint32_t* tslot = reinterpret_cast<uint32_t*>(idle + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     volatile int* never = abort_flag + 1;                // stays 0
-    volatile int* stop = abort_flag + 2;                 // the softmax warps' common end
-    volatile int* last_word = abort_flag + 3;
-    volatile int* odd = abort_flag + 4;                  // [16] of the pieces with keys, in order: take it row by row
+    volatile int* last_word = abort_flag + 2;
+    volatile int* odd = abort_flag + 3;                  // [16] of the pieces with keys, in order: take it row by row
 
     const AttnArgs& a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -335,11 +397,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
         for (int i = 0; i < 2; ++i) {
             mbar_init(sfull + i, 1);
             mbar_init(pfull + i, 4);
+            mbar_init(phalf + i, 4);
             mbar_init(ofull + i, 1);
         }
         for (int i = 0; i < 16; ++i) odd[i] = 0;
+        for (int i = 0; i < kTaSegs; ++i) {
+            mbar_init(pfull_seg + i, 1);
+            mbar_init(pempty_seg + i, 8 + 1 + kTaLoaders);
+        }
         mbar_init(idle, 1);
-        *abort_flag = *never = *stop = 0;
+        *abort_flag = *never = 0;
         fence_barrier_init();
     }
     if (warp == 8) tc_alloc(tslot, 512);
@@ -351,23 +418,18 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
     pdl_wait();
     pdl_launch_dependents();
 
-    // Each warp's walk and piece live in shared memory (all lanes write the
-    // same words): registers are for the softmax's rows.
-    __shared__ TaWalk walks[kTaThreads / 32];
-    __shared__ TaSeg segs[kTaThreads / 32];
-    TaWalk& w = walks[warp];
-    TaSeg& e = segs[warp];
-    w = ta_start(g);
-    __syncwarp();
-    auto next = [&]() {
-        TaWalk wn = w;
-        TaSeg en;
+    __shared__ TaSeg segs[kTaSegs];
+    // Every working warp goes through the parts in order: told_part() waits for the
+    // next one, drop() frees its place.
+    uint32_t part_no = 0;
+    auto told_part = [&]() {
+        return __all_sync(0xFFFFFFFFu,
+                          ta_wait(pfull_seg + part_no % kTaSegs, (part_no / kTaSegs) & 1, abort_flag));
+    };
+    auto drop = [&]() {
         __syncwarp();
-        const bool more = ta_next(g, wn, en);
-        w = wn;
-        e = en;
-        __syncwarp();
-        return more;
+        if (lane == 0) mbar_arrive(pempty_seg + part_no % kTaSegs);
+        ++part_no;
     };
     auto give_up = [&]() {
         *abort_flag = 1;
@@ -375,7 +437,11 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
     };
 
     if (warp >= 8) {
+    // Registers go to the softmax, which holds a row of S: 256 x 184 + 128 x 120
+    // of the 384 x 168 that the kernel starts with (checked at setup).
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     if (warp > 8) {
+        if (warp < 9 + kTaLoaders) {
         // ---- copies ----
         const int lw = warp - 9;
         uint32_t u = 0;                                  // tiles begun
@@ -407,11 +473,12 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 if (lane == 0) mbar_arrive(full + st);
             }
         };
-        while (ok && next()) {
+        while (ok && (ok = told_part())) {
+            const TaSeg& e = segs[part_no % kTaSegs];
+            if (!e.more) break;
             const int64_t ho = (int64_t)e.hk * a.kv.head_stride;
             // Keys that every row of the unit sees: tiles inside need no look.
-            const int t0 = (int)((int64_t)e.rt * kTaRows / a.group);
-            const int t1 = min(e.n - 1, (int)(((int64_t)(e.rt + 1) * kTaRows - 1) / a.group));
+            const int t0 = e.t0, t1 = e.t0 + (e.g0 + e.n_rows - 1) / a.group;
             int ilo, ihi, x0;
             seen_range(a, e.len, e.n, t1, ilo, x0);
             seen_range(a, e.len, e.n, t0, x0, ihi);
@@ -518,17 +585,41 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 }
             }
             if (nt > 0) ++seg_no;
+            drop();
         }
         cp_async_wait<0>();
         signal(u);
         if (!ok) give_up();
+        } else {
+            // ---- the walk over this CTA's parts ----
+            TaWalk w = ta_start(g);
+            for (uint32_t n = 0;; ++n) {
+                TaSeg e;
+                ta_next(g, w, e);
+                if (n >= kTaSegs && !__all_sync(0xFFFFFFFFu, ta_wait(pempty_seg + n % kTaSegs, (n / kTaSegs - 1) & 1,
+                                                                     abort_flag))) {
+                    give_up();
+                    break;
+                }
+                if (lane == 0) {
+                    segs[n % kTaSegs] = e;
+                    mbar_arrive(pfull_seg + n % kTaSegs);
+                }
+                __syncwarp();
+                if (!e.more) break;
+            }
+        }
     } else {
         // ---- products ----
         uint32_t u = 0, np[2] = {0, 0};                  // ring tiles used, P's waited for
         int seg_no = 0;
         bool ok = true;
-        while (ok && next()) {
-            if (e.nt == 0) continue;
+        while (ok && (ok = told_part())) {
+            const TaSeg& e = segs[part_no % kTaSegs];
+            if (!e.more) break;
+            const int nt = e.nt;
+            drop();
+            if (nt == 0) continue;
             if (lane == 0) {
                 auto wait = [&](uint64_t* bar, uint32_t par) {
                     if (ok && !ta_wait(bar, par, abort_flag)) ok = false;
@@ -550,23 +641,29 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                     scores(1, u % NS);
                     tc_commit(empty + u % NS);
                 }
-                for (int i = 0; i < e.nt && ok; ++i) {
+                for (int i = 0; i < nt && ok; ++i) {
                     const uint32_t uv = u + 1, uk = u + 2;
                     wait(full + uv % NS, (uv / NS) & 1);
 #pragma unroll
                     for (int acc = 0; acc < 2; ++acc) {
+                        auto weighted = [&](int kk) {
+                            tc_mma_f16_ta(tmem + kColO + 128u * acc, tmem + 128u * acc + 8u * kk,
+                                          tc_sdesc_sw128_nmajor(sRing + (uv % NS) * kTile + 2048u * kk, kHalf),
+                                          g.idesc_o, (i | kk) != 0);
+                        };
+                        wait(phalf + acc, np[acc] & 1);
+                        if (ok)
+#pragma unroll
+                            for (int kk = 0; kk < kTaKeys / 32; ++kk) weighted(kk);
                         wait(pfull + acc, np[acc] & 1);
                         ++np[acc];
                         if (ok) {
 #pragma unroll
-                            for (int kk = 0; kk < kTaKeys / 16; ++kk)
-                                tc_mma_f16_ta(tmem + kColO + 128u * acc, tmem + 128u * acc + 8u * kk,
-                                              tc_sdesc_sw128_nmajor(sRing + (uv % NS) * kTile + 2048u * kk, kHalf),
-                                              g.idesc_o, (i | kk) != 0);
+                            for (int kk = kTaKeys / 32; kk < kTaKeys / 16; ++kk) weighted(kk);
                             if (acc == 1) tc_commit(empty + uv % NS);
-                            if (i + 1 == e.nt) tc_commit(ofull + acc);
+                            if (i + 1 == nt) tc_commit(ofull + acc);
                         }
-                        if (i + 1 < e.nt) {
+                        if (i + 1 < nt) {
                             if (acc == 0) wait(full + uk % NS, (uk / NS) & 1);
                             if (ok) {
                                 scores(acc, uk % NS);
@@ -589,6 +686,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
         __syncwarp();
     }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ---- softmax: a thread has row `row` of accumulator `acc` ----
         const int acc = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -598,19 +696,27 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
         bool ok = true;
         const bool neg = a.scale_log2 < 0.f, flat = a.scale_log2 == 0.f;
         const float sc = flat ? 1.f : fabsf(a.scale_log2);
-        while (next()) {
-            const int64_t r0 = (int64_t)e.rt * kTaRows + acc * 128;      // of the sequence's rows
-            const int64_t n_rows = (int64_t)e.n * a.group;
+        for (;; drop()) {
+            // The eight warps go on, or end, together.
+            if (!told_part()) ok = false;
+            if (!ok) give_up();
+            if (!all_softmax(ok)) break;
+            const TaSeg& e = segs[part_no % kTaSegs];
+            if (!e.more) break;
+            const int xr = acc * 128 + row;              // of the unit's rows
             if (e.nt > 0) {
-                // Queries of this accumulator.
-                for (int x = threadIdx.x & 127; x < 128 * CH; x += 128) {
-                    const int rr = x / CH, ch = x % CH;
-                    const int64_t r = r0 + rr, t = r / a.group;
-                    const bool in = r < n_rows && 8 * ch < D;
-                    const int64_t at = in ? (e.first + t) * a.q_stride + (int64_t)(e.hk * a.group + (int)(r - t * a.group)) * D + 8 * ch : 0;
+                // Queries of this accumulator: a thread's chunk of every
+                // 128 / CH-th row.
+                const int ch = (int)(threadIdx.x & 127) % CH;
+#pragma unroll 4
+                for (int rr = (int)(threadIdx.x & 127) / CH; rr < 128; rr += 128 / CH) {
+                    const int x = acc * 128 + rr, gx = e.g0 + x, t = gx / a.group, gh = gx - t * a.group;
+                    const bool in = x < e.n_rows && 8 * ch < D;
+                    const T* src = static_cast<const T*>(a.q) +
+                                   (in ? (e.first + e.t0 + t) * a.q_stride + (int64_t)(e.hk * a.group + gh) * D + 8 * ch : 0);
                     cp_async16(sQ + acc * kTile + (uint32_t)(ch >> 3) * kHalf +
                                    (uint32_t)(rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)),
-                               static_cast<const T*>(a.q) + at, in);
+                               src, in);
                 }
                 cp_async_commit();
                 cp_async_wait<0>();
@@ -620,61 +726,52 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 ++q_no;
             }
             // Keys that this row sees, and that all rows of the warp see.
+            const bool real = xr < e.n_rows;
+            const int tr = (e.g0 + xr) / a.group;        // its token, from the unit's first
             int lo = 0, hi = 0;
-            const int64_t r = r0 + row;
-            if (r < n_rows) seen_range(a, e.len, e.n, (int)(r / a.group), lo, hi);
-            int wlo = r < n_rows ? lo : 0, whi = r < n_rows ? hi : INT32_MAX;
+            if (real) seen_range(a, e.len, e.n, e.t0 + tr, lo, hi);
+            int wlo = real ? lo : 0, whi = real ? hi : INT32_MAX;
             for (int x = 16; x; x >>= 1) {
                 wlo = max(wlo, __shfl_xor_sync(0xFFFFFFFFu, wlo, x));
                 whi = min(whi, __shfl_xor_sync(0xFFFFFFFFu, whi, x));
             }
+            T* out = static_cast<T*>(a.out) + (e.first + e.t0 + tr) * a.o_stride +
+                     (int64_t)(e.hk * a.group + (e.g0 + xr - tr * a.group)) * D;
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < e.nt && ok; ++i) {
                 ok = __all_sync(0xFFFFFFFFu, ta_wait(sfull + acc, ns & 1, abort_flag));
                 ++ns;
                 if (!ok) break;
                 tc_fence_after();
-                // The row's 128 scores, 32 columns at a time: once for the
-                // maximum, then (the first half read again: registers) for
-                // the weights, which go where the scores were just taken from.
-                const int j = e.j0 + i * kTaKeys;
-                const int c0 = lo - j, c1 = hi - j;
-                const bool masked = j < wlo || j + kTaKeys > whi;
-                auto prepare = [&](float (&v)[32], int x) {
-                    if (neg || flat)
+                float v[4][32];                          // the row's 128 scores
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) v[y] = neg ? -v[y] : 0.f * v[y];
-                    if (masked)
+                for (int x = 0; x < 4; ++x) tc_ld32(tS + 32u * x, v[x]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tc_wait_ld(v[x]);
+                const int j = e.j0 + i * kTaKeys;
+                if (neg || flat) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) v[x][y] = neg ? -v[x][y] : 0.f * v[x][y];
+                }
+                if (j < wlo || j + kTaKeys > whi) {
+                    const int c0 = lo - j, c1 = hi - j;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
 #pragma unroll
                         for (int y = 0; y < 32; ++y)
-                            if (32 * x + y < c0 || 32 * x + y >= c1) v[y] = -INFINITY;
-                };
-                auto largest = [&](const float (&v)[32]) {
-                    float m0 = v[0], m1 = v[1];
+                            if (32 * x + y < c0 || 32 * x + y >= c1) v[x][y] = -INFINITY;
+                }
+                float mx[8];
 #pragma unroll
-                    for (int y = 2; y < 32; y += 2) {
-                        m0 = fmaxf(m0, v[y]);
-                        m1 = fmaxf(m1, v[y + 1]);
-                    }
-                    return fmaxf(m0, m1);
-                };
-                float sa[32], sb[32], sd[32];
-                tc_ld32(tS, sa);
-                tc_wait_ld(sa);
-                tc_ld32(tS + 32u, sb);
-                prepare(sa, 0);
-                float top = largest(sa);
-                tc_wait_ld(sb);
-                tc_ld32(tS + 64u, sd);
-                prepare(sb, 1);
-                top = fmaxf(top, largest(sb));
-                tc_wait_ld(sd);
-                tc_ld32(tS + 96u, sb);
-                prepare(sd, 2);
-                top = fmaxf(top, largest(sd));
-                tc_wait_ld(sb);
-                prepare(sb, 3);
-                top = fmaxf(top, largest(sb)) * sc;
+                for (int x = 0; x < 8; ++x) {
+                    mx[x] = v[0][x];
+#pragma unroll
+                    for (int y = 8; y < 128; y += 8) mx[x] = fmaxf(mx[x], v[(x + y) >> 5][(x + y) & 31]);
+                }
+                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sc;
                 float f = 1.f;
                 if (i == 0) {
                     m = top;
@@ -686,41 +783,37 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 if (__any_sync(0xFFFFFFFFu, f != 1.f)) {
                     // S came after the last P V, so the sums are at rest.
 #pragma unroll 1
-                    for (int x = 0; x < DP / 32; ++x) {
-                        float o[32];
-                        uint32_t ow[32];
-                        tc_ld32(tO + 32u * x, o);
-                        tc_wait_ld(o);
+                    for (int x = 0; x < DP / 16; ++x) {
+                        uint32_t o[16];
+                        tc_ld16(tO + 16u * x, o);
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) ow[y] = __float_as_uint(o[y] * f);
-                        tc_st32(tO + 32u * x, ow);
+                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                        tc_st16(tO + 16u * x, o);
                     }
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
-                auto weights = [&](const float (&v)[32], int x) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
                     uint32_t pw[16];
 #pragma unroll
                     for (int y = 0; y < 16; ++y) {
-                        float2 t = ffma2(make_float2(v[2 * y], v[2 * y + 1]), sc2, mu2);
+                        float2 t = ffma2(make_float2(v[x][2 * y], v[x][2 * y + 1]), sc2, mu2);
                         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(t.x));
                         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(t.y));
                         sum[y & 1] = fadd2(sum[y & 1], t);
                         pw[y] = Elem<T>::pack(t.x, t.y);
                     }
                     tc_st16(tS + 16u * x, pw);
-                };
-                tc_ld32(tS, sa);
-                tc_wait_ld(sa);
-                prepare(sa, 0);
-                weights(sa, 0);
-                tc_ld32(tS + 32u, sa);
-                tc_wait_ld(sa);
-                prepare(sa, 1);
-                weights(sa, 1);
-                weights(sd, 2);
-                weights(sb, 3);
+                    if (x == 1) {
+                        // The first 64 keys' weights: their product may begin.
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(phalf + acc);
+                    }
+                }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tc_wait_st();
                 tc_fence_before();
@@ -731,19 +824,13 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 ok = __all_sync(0xFFFFFFFFu, ta_wait(ofull + acc, (q_no - 1) & 1, abort_flag));
                 tc_fence_after();
             }
-            // After a wait that gave up, the warp still meets the others at the
-            // barriers below and they end together.
-            if (!ok) give_up();
             // The copying warps' marks on this piece reach here through the
             // products' barriers; they are at most five pieces ahead.
             const bool rows_apart = e.nt > 0 && odd[(q_no - 1) & 15] != 0;
-            float* slot = g.ws + (2 * (int64_t)blockIdx.x + e.slot) * ta_slot(DP);
+            float* slot = g.ws + (int64_t)e.slot * ta_slot(DP);
             if (e.pieces == 1) {
                 if (!rows_apart) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;
-                    const int64_t t = r / a.group;
-                    T* out = static_cast<T*>(a.out) + (e.first + t) * a.o_stride +
-                             (int64_t)(e.hk * a.group + (int)(r - t * a.group)) * D;
 #pragma unroll
                     for (int x = 0; x < DP / 32; ++x) {
                         float o[32];
@@ -756,7 +843,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                             float v[8];
 #pragma unroll
                             for (int z = 0; z < 8; ++z) v[z] = e.nt > 0 ? o[8 * y + z] * inv : 0.f;
-                            if (r < n_rows && 32 * x + 8 * y < D) *reinterpret_cast<uint4*>(out + 32 * x + 8 * y) = pack8<T>(v);
+                            if (real && 32 * x + 8 * y < D) *reinterpret_cast<uint4*>(out + 32 * x + 8 * y) = pack8<T>(v);
                         }
                     }
                 }
@@ -764,7 +851,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 // A piece: sums as [column / 4][row][4], so a warp's stores are
                 // 512 contiguous bytes.  The mark for a row-by-row unit is a
                 // weights' sum of -1.
-                const int rr = acc * 128 + row;
+                const int rr = xr;
 #pragma unroll
                 for (int x = 0; x < DP / 32; ++x) {
                     float o[32];
@@ -789,64 +876,65 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
             if (e.pieces > 1 && *last_word) {
                 __threadfence();
                 if (threadIdx.x == 0) g.cnt[e.c_lo] = 0;
-                const int rr = acc * 128 + row;
+                // Piece 0 may be in its CTA's second slot, the others are in
+                // their CTAs' first.
+                auto piece = [&](int p) {
+                    return g.ws + (int64_t)(p ? 2 * (e.c_lo + p) : e.slot0) * ta_slot(DP) + xr * 4;
+                };
+                constexpr int kM = kTaRows * DP;         // maxima, then sums
                 float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
                 for (int p = 0; p < e.pieces; ++p) {
-                    const float* sp = g.ws + ta_piece(w, e, p) * ta_slot(DP) + kTaRows * DP + rr;
+                    const float* sp = piece(p) - 3 * xr + kM;
                     top = fmaxf(top, __ldcg(sp));
                     if (__ldcg(sp + kTaRows) == -1.f) apart = true;
                 }
                 const float mu = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
                 for (int p = 0; p < e.pieces; ++p) {
-                    const float* sp = g.ws + ta_piece(w, e, p) * ta_slot(DP) + kTaRows * DP + rr;
+                    const float* sp = piece(p) - 3 * xr + kM;
                     sum += exp2f(__ldcg(sp) - mu) * __ldcg(sp + kTaRows);
                 }
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                const int64_t t = r / a.group;
-                T* out = static_cast<T*>(a.out) + (e.first + t) * a.o_stride +
-                         (int64_t)(e.hk * a.group + (int)(r - t * a.group)) * D;
 #pragma unroll 1
-                for (int x = 0; x < DP / 32; ++x) {
-                    float4 o[8];
+                for (int x = 0; x < DP / 64; ++x) {
+                    float4 o[16];
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int y = 0; y < 16; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
                     for (int p = 0; p < e.pieces; ++p) {
-                        const float* sp = g.ws + ta_piece(w, e, p) * ta_slot(DP);
-                        const float wt = exp2f(__ldcg(sp + kTaRows * DP + rr) - mu);
+                        const float* sp = piece(p);
+                        const float wt = exp2f(__ldcg(sp - 3 * xr + kM) - mu);
+                        float4 v[16];
+#pragma unroll
+                        for (int y = 0; y < 16; ++y)
+                            v[y] = __ldcg(reinterpret_cast<const float4*>(sp + (16 * x + y) * (4 * kTaRows)));
                         if (wt == 0.f) continue;         // no keys: the slot's sums were not written
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(sp + ((8 * x + y) * kTaRows + rr) * 4));
-                            o[y].x += wt * v.x;
-                            o[y].y += wt * v.y;
-                            o[y].z += wt * v.z;
-                            o[y].w += wt * v.w;
+                        for (int y = 0; y < 16; ++y) {
+                            o[y].x += wt * v[y].x;
+                            o[y].y += wt * v[y].y;
+                            o[y].z += wt * v[y].z;
+                            o[y].w += wt * v[y].w;
                         }
                     }
-                    if (r < n_rows)
+                    if (real)
 #pragma unroll
-                        for (int y = 0; y < 8; ++y)
-                            if (32 * x + 4 * y < D)
-                                *reinterpret_cast<uint2*>(out + 32 * x + 4 * y) =
+                        for (int y = 0; y < 16; ++y)
+                            if (64 * x + 4 * y < D)
+                                *reinterpret_cast<uint2*>(out + 64 * x + 4 * y) =
                                     make_uint2(Elem<T>::pack(o[y].x * inv, o[y].y * inv),
                                                Elem<T>::pack(o[y].z * inv, o[y].w * inv));
                 }
             }
             bar_softmax();               // everyone has read this piece's mark and the word above
-            if (threadIdx.x == 0) {
-                if (e.nt > 0) odd[(q_no - 1) & 15] = 0;
-                *stop = *abort_flag;
-            }
-            bar_softmax();
-            if (*stop) break;
+            if (threadIdx.x == 0 && e.nt > 0) odd[(q_no - 1) & 15] = 0;
             if (apart) {
-                for (int x = warp; x < kTaRows; x += 8) {
-                    const int64_t rx = (int64_t)e.rt * kTaRows + x;
-                    if (rx >= n_rows) break;
-                    const int t = (int)(rx / a.group);
+                for (int x = warp; x < e.n_rows; x += 8) {
+                    const int t = (e.g0 + x) / a.group;
                     int l0, h0;
-                    seen_range(a, e.len, e.n, t, l0, h0);
-                    attend_row<T>(a, e.s, e.first + t, e.hk * a.group + (int)(rx - (int64_t)t * a.group), l0, h0);
+                    seen_range(a, e.len, e.n, e.t0 + t, l0, h0);
+                    attend_row<T>(a, e.s, e.first + e.t0 + t, e.hk * a.group + (e.g0 + x - t * a.group), l0, h0);
                 }
             }
         }

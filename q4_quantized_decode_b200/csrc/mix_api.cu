@@ -366,7 +366,6 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
         g.ws = cx.attn_ws;
         g.cnt = cx.attn_cnt;
         g.min_rows = few ? kSplitRowsMax : 0;
-        g.min_cost = 768;
         const int dp = kv->head_dim <= 64 ? 64 : 128;
         // Boxes of a page each (of 128 tokens in larger pages), where pages of
         // a power of two from 8 on divide a tile or are divided by it.
