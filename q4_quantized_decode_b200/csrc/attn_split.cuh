@@ -29,7 +29,8 @@ namespace q4 {
 constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = 32 * kSplitWarps;
 constexpr int kSplitKeys = 16;                          // keys of a warp's tile
-constexpr int kSplitBlock = kSplitKeys * kSplitWarps;   // keys of a CTA's block
+constexpr int kSplitBlock = kSplitKeys * kSplitWarps;   // keys of a CTA's step
+constexpr int kSplitGroup = 4 * kSplitBlock;            // keys of a group
 constexpr int kSplitRows = 16;
 constexpr int kSplitStages = 3;
 // CTAs of an SM at each padded head size (shared memory: stages * 4 warps * 16
@@ -46,15 +47,15 @@ struct SplitAttnArgs {
     float* ws;          // [2 * gridDim.x] slots
     int* cnt;           // [gridDim.x] arrivals, zero between calls
     int max_rows;       // rows (tokens * group) of a sequence that this kernel takes; 0: any
-    int min_blocks;     // blocks of a CTA, at least
 };
 
 // The units of sequence s: `tiles` row tiles (times the key heads), each of
-// `blocks` key blocks (the count for the longest range of its rows).
+// `groups` key groups (the count for the longest range of its rows).
 struct SeqWork {
     int64_t first;      // first row of the batch
     int n, len;         // new tokens, tokens in the cache
-    int tiles, blocks;
+    int tiles, groups;
+    __device__ __forceinline__ int64_t all(int heads) const { return (int64_t)tiles * groups * heads; }
     int lo;             // first key that any row sees
 };
 
@@ -64,14 +65,14 @@ __device__ __forceinline__ SeqWork seq_work(const SplitAttnArgs& g, int s) {
     seq_rows(a.batch, s, w.first, w.n);
     w.len = a.batch.len[s];
     const int64_t rows = (int64_t)w.n * a.group;
-    w.tiles = w.blocks = w.lo = 0;
+    w.tiles = w.groups = w.lo = 0;
     if (w.n == 0 || (g.max_rows && rows > g.max_rows)) return w;
     w.tiles = (int)((rows + kSplitRows - 1) / kSplitRows);
     int hi, lo1;
     seen_range(a, w.len, w.n, 0, w.lo, hi);             // the first row starts lowest
     seen_range(a, w.len, w.n, w.n - 1, lo1, hi);        // the last one ends highest
     w.lo = w.lo / kSplitBlock * kSplitBlock;
-    w.blocks = hi > w.lo ? (hi - w.lo + kSplitBlock - 1) / kSplitBlock : 1;   // an empty range is one block
+    w.groups = hi > w.lo ? (hi - w.lo + kSplitGroup - 1) / kSplitGroup : 1;   // an empty range is one group
     return w;
 }
 
@@ -92,30 +93,36 @@ __global__ void __launch_bounds__(kSplitThreads, split_ctas_per_sm(DP)) attn_spl
     pdl_wait();
     pdl_launch_dependents();
 
-    // Blocks of all units, and this CTA's run of them.
+    // Groups of all units, and this CTA's run of them.
     const int nh = a.kv.n_heads, n_seqs = a.batch.n_seqs;
-    int64_t mine = 0;
-    for (int s = lane; s < n_seqs; s += 32) {
-        const SeqWork w = seq_work(g, s);
-        mine += (int64_t)w.tiles * w.blocks * nh;
+    SeqWork w;
+    w.tiles = w.groups = 0;
+    int64_t total = 0, first_all = 0;                     // first_all: lane's sequence of the first 32
+    for (int q = lane; q < n_seqs; q += 32) {
+        const SeqWork x = seq_work(g, q);
+        total += x.all(nh);
+        if (q == lane) {
+            w = x;
+            first_all = x.all(nh);
+        }
     }
-    for (int x = 16; x; x >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, x);
-    const int64_t total = mine;
-    int64_t runs = (total + g.min_blocks - 1) / g.min_blocks;
-    if (runs > gridDim.x) runs = gridDim.x;
-    if ((int64_t)blockIdx.x >= runs) return;
-    auto run_start = [&](int64_t c) { return c * total / runs; };
-    const int64_t b0 = run_start(blockIdx.x), b1 = run_start((int64_t)blockIdx.x + 1);
+    for (int x = 16; x; x >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, x);
+    const int runs = (int)min((int64_t)gridDim.x, total);
+    const int me = (int)blockIdx.x;
+    if (me >= runs) return;
+    const double ratio = (double)total / (double)runs;    // groups of a run; the same cuts in every CTA
+    auto run_start = [&](int c) { return c >= runs ? total : (int64_t)((double)c * ratio); };
+    const int64_t b0 = run_start(me), b1 = run_start(me + 1);
 
-    // The sequence of block b0: prefix sums of 32 sequences at a time.
-    int64_t seq_base = 0;                                 // blocks before sequence s
+    // The sequence of group b0: prefix sums of 32 sequences at a time.
+    int64_t seq_base = 0;                                 // groups before sequence s
     int s = 0;
     for (int c0 = 0; c0 < n_seqs; c0 += 32) {
-        int64_t x = 0;
-        if (c0 + lane < n_seqs) {
-            const SeqWork w = seq_work(g, c0 + lane);
-            x = (int64_t)w.tiles * w.blocks * nh;
+        if (c0 > 0) {
+            w.tiles = w.groups = 0;
+            if (c0 + lane < n_seqs) w = seq_work(g, c0 + lane);
         }
+        const int64_t x = c0 > 0 ? w.all(nh) : first_all;
         int64_t p = x;
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t y = __shfl_up_sync(0xFFFFFFFFu, p, d);
@@ -126,21 +133,26 @@ __global__ void __launch_bounds__(kSplitThreads, split_ctas_per_sm(DP)) attn_spl
             const int l = __ffs((int)past) - 1;
             s = c0 + l;
             seq_base += __shfl_sync(0xFFFFFFFFu, p - x, l);
+            w.first = __shfl_sync(0xFFFFFFFFu, w.first, l);
+            w.n = __shfl_sync(0xFFFFFFFFu, w.n, l);
+            w.len = __shfl_sync(0xFFFFFFFFu, w.len, l);
+            w.tiles = __shfl_sync(0xFFFFFFFFu, w.tiles, l);
+            w.groups = __shfl_sync(0xFFFFFFFFu, w.groups, l);
+            w.lo = __shfl_sync(0xFFFFFFFFu, w.lo, l);
             break;
         }
         seq_base += __shfl_sync(0xFFFFFFFFu, p, 31);
     }
 
-    SeqWork w = seq_work(g, s);
     for (int64_t b = b0; b < b1;) {
-        while (b >= seq_base + (int64_t)w.tiles * w.blocks * nh && s + 1 < n_seqs) {     // sequences without blocks are passed
-            seq_base += (int64_t)w.tiles * w.blocks * nh;
+        while (b >= seq_base + w.all(nh) && s + 1 < n_seqs) {          // sequences without groups are passed
+            seq_base += w.all(nh);
             w = seq_work(g, ++s);
         }
-        const int64_t unit = (b - seq_base) / w.blocks;
-        const int64_t ub = seq_base + unit * w.blocks;                 // the unit's first block
-        const int64_t be = b1 < ub + w.blocks ? b1 : ub + w.blocks;
-        const int rt = (int)(unit / nh), hk = (int)(unit - (int64_t)rt * nh);
+        const int64_t unit = div_floor(b - seq_base, max(1, w.groups));
+        const int64_t ub = seq_base + unit * w.groups;                 // the unit's first group
+        const int64_t be = b1 < ub + w.groups ? b1 : ub + w.groups;
+        const int rt = (int)div_floor(unit, nh), hk = (int)(unit - (int64_t)rt * nh);
         const int n_rows = min(kSplitRows, w.n * a.group - rt * kSplitRows);
 
         // Ranges: this thread's rows lane / 4 and that + 8, the tile's union
@@ -168,8 +180,9 @@ __global__ void __launch_bounds__(kSplitThreads, split_ctas_per_sm(DP)) attn_spl
             ihi = min(ihi, __shfl_xor_sync(0xFFFFFFFFu, ihi, x));
         }
         // This warp's tiles: keys k0 + 64 i .. + 16, i in [0, nt).
-        int nt = (int)(be - b);
-        int k0 = w.lo + (int)(b - ub) * kSplitBlock + warp * kSplitKeys;
+        const int from = w.lo + (int)(b - ub) * kSplitGroup;
+        const int nt = min((int)(be - b) * (kSplitGroup / kSplitBlock), max(0, (thi - from + kSplitBlock - 1) / kSplitBlock));
+        const int k0 = from + warp * kSplitKeys;
 
         // Key `lane & 15` of tile i: its element offset, or -1.
         const int64_t ho = (int64_t)hk * a.kv.head_stride;
@@ -374,7 +387,7 @@ __global__ void __launch_bounds__(kSplitThreads, split_ctas_per_sm(DP)) attn_spl
             }
         }
         __syncthreads();
-        const bool whole = b == ub && be == ub + w.blocks;
+        const bool whole = b == ub && be == ub + w.groups;
         const bool first_seg = b == b0;
         float* slot = g.ws + ((int64_t)blockIdx.x * 2 + (first_seg ? 0 : 1)) * split_slot(DP);
         auto store_out = [&](int row, int c4, float4 v) {
@@ -416,14 +429,14 @@ __global__ void __launch_bounds__(kSplitThreads, split_ctas_per_sm(DP)) attn_spl
         if (!whole) {
             // The unit's pieces are in the CTAs c_lo .. c_hi; its count is kept
             // under c_lo, whose run no other unit leaves at its end.
-            auto cta_of = [&](int64_t blk) {
-                int64_t c = blk * runs / total;
-                while (run_start(c + 1) <= blk) ++c;
-                while (run_start(c) > blk) --c;
+            auto cta_of = [&](int64_t grp) {
+                int c = min(runs - 1, (int)((double)grp / ratio));
+                while (c + 1 < runs && run_start(c + 1) <= grp) ++c;
+                while (c > 0 && run_start(c) > grp) --c;
                 return c;
             };
-            const int64_t c_lo = cta_of(ub), c_hi = cta_of(ub + w.blocks - 1);
-            const int pieces = (int)(c_hi - c_lo) + 1;
+            const int c_lo = cta_of(ub), c_hi = cta_of(ub + w.groups - 1);
+            const int pieces = c_hi - c_lo + 1;
             __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) last_word = atom_add_acq_rel_gpu(g.cnt + c_lo, 1) == pieces - 1;
@@ -431,46 +444,50 @@ __global__ void __launch_bounds__(kSplitThreads, split_ctas_per_sm(DP)) attn_spl
             if (last_word) {
                 __threadfence();
                 if (threadIdx.x == 0) g.cnt[c_lo] = 0;
-                // Shared memory: each piece's slot, its rows' weights
-                // [pieces][16], the rows' 1 / sum.
-                int* slots = reinterpret_cast<int*>(split_smem_raw);
-                float* wts = reinterpret_cast<float*>(slots + gridDim.x);
+                // Every piece but the first begins its CTA's run: the first slot.
+                const int64_t slot0 = 2 * (int64_t)c_lo + (run_start(c_lo) >= ub ? 0 : 1);
+                auto piece = [&](int p) { return g.ws + (p ? 2 * (int64_t)(c_lo + p) : slot0) * split_slot(DP); };
+                // Shared memory: the pieces' rows' weights [pieces][16], the
+                // rows' 1 / sum.
+                float* wts = reinterpret_cast<float*>(split_smem_raw);
                 float* invs = wts + gridDim.x * kSplitRows;
-                for (int p = threadIdx.x; p < pieces; p += kSplitThreads)
-                    slots[p] = (int)(2 * (c_lo + p) + (run_start(c_lo + p) >= ub ? 0 : 1));
-                __syncthreads();
                 {
                     // Eight threads a row.
                     const int row = threadIdx.x >> 3, part = threadIdx.x & 7;
                     float mx = -INFINITY, ls = 0.f;
                     if (row < n_rows)
+#pragma unroll 4
                         for (int p = part; p < pieces; p += 8) {
-                            const float v = __ldcg(g.ws + (int64_t)slots[p] * split_slot(DP) + kSplitRows * DP + row);
+                            const float v = __ldcg(piece(p) + kSplitRows * DP + row);
+                            const float sum = __ldcg(piece(p) + kSplitRows * DP + kSplitRows + row);
                             wts[p * kSplitRows + row] = v;
-                            mx = fmaxf(mx, v);
+                            const float mn = fmaxf(mx, v), mu = mn == -INFINITY ? 0.f : mn;
+                            ls = ls * exp2f(mx - mu) + sum * exp2f(v - mu);
+                            mx = mn;
                         }
 #pragma unroll
-                    for (int x = 1; x < 8; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+                    for (int x = 1; x < 8; x <<= 1) {
+                        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, mx, x), l2 = __shfl_xor_sync(0xFFFFFFFFu, ls, x);
+                        const float mn = fmaxf(mx, m2), mu = mn == -INFINITY ? 0.f : mn;
+                        ls = ls * exp2f(mx - mu) + l2 * exp2f(m2 - mu);
+                        mx = mn;
+                    }
                     const float mu = mx == -INFINITY ? 0.f : mx;
                     if (row < n_rows)
-                        for (int p = part; p < pieces; p += 8) {
-                            const float wt = exp2f(wts[p * kSplitRows + row] - mu);
-                            wts[p * kSplitRows + row] = wt;
-                            ls += wt * __ldcg(g.ws + (int64_t)slots[p] * split_slot(DP) + kSplitRows * DP + kSplitRows + row);
-                        }
-#pragma unroll
-                    for (int x = 1; x < 8; x <<= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, x);
+                        for (int p = part; p < pieces; p += 8)
+                            wts[p * kSplitRows + row] = exp2f(wts[p * kSplitRows + row] - mu);
                     if (part == 0) invs[row] = ls == 0.f ? 0.f : 1.f / ls;
                 }
                 __syncthreads();
                 for (int x = threadIdx.x; x < n_rows * (DP / 4); x += kSplitThreads) {
                     const int row = x / (DP / 4), c4 = x % (DP / 4);
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+                    const float* at = g.ws + row * DP + 4 * c4;
+#pragma unroll 16
                     for (int p = 0; p < pieces; ++p) {
                         const float wt = wts[p * kSplitRows + row];
-                        const float4 u = __ldcg(reinterpret_cast<const float4*>(g.ws + (int64_t)slots[p] * split_slot(DP) +
-                                                                                row * DP + 4 * c4));
+                        const float4 u = __ldcg(reinterpret_cast<const float4*>(
+                            at + (p ? 2 * (int64_t)(c_lo + p) : slot0) * split_slot(DP)));
                         v.x += wt * u.x;
                         v.y += wt * u.y;
                         v.z += wt * u.z;

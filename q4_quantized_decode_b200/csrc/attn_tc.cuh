@@ -107,10 +107,6 @@ struct TaSeg {
     int slot, slot0;     // workspace slots of this piece and of the first
 };
 
-__device__ __forceinline__ int64_t div_floor(int64_t a, int b) {      // a >= 0, b > 0
-    return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 // Walks over a CTA's units (one warp, all lanes alike).
 struct TaWalk {
     double ratio;        // cost of a run

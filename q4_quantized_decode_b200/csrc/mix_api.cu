@@ -381,7 +381,6 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
     g.ws = cx.attn_ws;
     g.cnt = cx.attn_cnt;
     g.max_rows = many ? kSplitRowsMax : 0;
-    g.min_blocks = 2;
     return launch_status(h, f16 ? split_launch<__half>(g, cx.sms, st) : split_launch<__nv_bfloat16>(g, cx.sms, st), call);
 }
 

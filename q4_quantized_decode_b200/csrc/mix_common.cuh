@@ -107,6 +107,10 @@ __device__ __forceinline__ int find_seq(const int32_t* start, int n_seqs, int64_
     return -1;
 }
 
+__device__ __forceinline__ int64_t div_floor(int64_t a, int b) {      // a >= 0, b > 0
+    return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // A paged cache: token t of sequence s is in page table[s * table_stride +
 // t / page_size], at row t % page_size.  Strides in elements.
 struct KvArgs {
