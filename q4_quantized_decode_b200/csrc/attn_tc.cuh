@@ -15,7 +15,7 @@
 //   warps 9-10 the pages' rows into a ring of 128-key tiles, in the 128-byte
 //              swizzle that the products read (K as rows of K, V as an N-major
 //              operand): tiles that every row sees whole by tensor map, where
-//              pages of 8, 16, .. tokens allow it, the others by asynchronous
+//              pages of a multiple of 8 tokens allow it, the others by asynchronous
 //              16-byte copies, because pages may end anywhere in a tile and
 //              keys that no row sees have to be zeros.
 // Two products of 128 x 128 x head_dim for each accumulator and tile, 16384
@@ -64,7 +64,7 @@ struct TcAttnArgs {
     int* cnt;            // [gridDim.x] arrivals, zero between calls
     int min_rows;        // sequences of at most this many rows are another kernel's
     uint32_t idesc_s, idesc_o;
-    int box;             // tokens of a tensor-map box (8..128, page_size or 128), 0: no maps
+    int box;             // tokens of a tensor-map box (8..128, dividing page_size), 0: no maps
     CUtensorMap kmap, vmap;   // [page][head][token][element], boxes of 64 elements x `box` tokens
 };
 
@@ -484,35 +484,23 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
             // its part) a box; the others by 16-byte copies, which leave keys
             // that no row sees zero.
             auto by_map = [&](int j) { return g.box && j >= ilo && j + kTaKeys <= ihi; };
-            // Page of box lane / parts of the tile at j, or keys lane, lane + 32
-            // of this warp's.
-            const int parts = DP / 64, boxes = g.box ? kTaKeys / g.box : 0;
-            int pg = -1;
-            int64_t off[2] = {-1, -1};
-            bool page_bad = false;
+            // Pages of the next tile, as read (not yet checked, so nothing waits
+            // for them), with the rows in them: of boxes lane / parts (and that
+            // of lane + 32), or of keys lane, lane + 32 of this warp's; row -1 for
+            // a key that no row sees.
+            const int parts = DP / 64, items = g.box ? kTaKeys / g.box * parts : 0;
+            const int32_t* table = a.kv.table + (int64_t)seq * a.kv.table_stride;
+            int pg[2], pr[2] = {-1, -1};
             auto lookup = [&](int j) {
-                if (by_map(j)) {
-                    pg = 0;
-                    if (lane < boxes * parts) {
-                        int page, row;
-                        split_page(a.kv, j + (lane / parts) * g.box, page, row);
-                        pg = a.kv.table[(int64_t)seq * a.kv.table_stride + page];      // inside the columns: j < cap
-                        if ((unsigned)pg >= (unsigned)a.kv.n_pages) {
-                            set_device_error(a.err, kDevIndex);
-                            page_bad = true;
-                            pg = 0;
-                        }
-                    }
-                } else {
+                const bool map = by_map(j);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int key = j + 64 * lw + 32 * y + lane;
-                        off[y] = -1;
-                        if (key >= tlo && key < thi) {
-                            off[y] = token_offset(a.kv, seq, key, a.err);
-                            if (off[y] < 0) page_bad = true;
-                            else off[y] += ho;
-                        }
+                for (int y = 0; y < 2; ++y) {
+                    const int key = map ? j + (lane + 32 * y) / parts * g.box : j + 64 * lw + 32 * y + lane;
+                    pr[y] = -1;
+                    if (map ? lane + 32 * y < items : key >= tlo && key < thi) {
+                        int page;
+                        split_page(a.kv, key, page, pr[y]);
+                        pg[y] = table[page];             // inside the columns: key < cap
                     }
                 }
             };
@@ -520,10 +508,27 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
             for (int i = 0; i < nt && ok; ++i) {
                 const int j = j_first + i * kTaKeys;
                 const bool mapped = by_map(j);
-                const int pg_now = pg;
-                const int64_t off0 = off[0], off1 = off[1];
-                if (page_bad) odd[seg_no & 15] = 1;
-                page_bad = false;
+                int pgn[2], prn[2];                      // of this tile, checked
+                int64_t off0 = -1, off1 = -1;
+                bool page_bad = false;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    prn[y] = pr[y];
+                    pgn[y] = pr[y] < 0 ? 0 : pg[y];
+                    if ((unsigned)pgn[y] >= (unsigned)a.kv.n_pages) {
+                        page_bad = true;
+                        pgn[y] = 0;
+                        if (!mapped) prn[y] = -1;
+                    }
+                }
+                if (!mapped) {
+                    if (prn[0] >= 0) off0 = (int64_t)pgn[0] * a.kv.page_stride + (int64_t)prn[0] * a.kv.token_stride + ho;
+                    if (prn[1] >= 0) off1 = (int64_t)pgn[1] * a.kv.page_stride + (int64_t)prn[1] * a.kv.token_stride + ho;
+                }
+                if (page_bad) {
+                    set_device_error(a.err, kDevIndex);
+                    odd[seg_no & 15] = 1;
+                }
                 if (i + 1 < nt) lookup(j + kTaKeys);     // the next tile's pages, on their way meanwhile
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++u) {
@@ -549,13 +554,14 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                             else mbar_arrive(full + st);
                         }
                         __syncwarp();
-                        if (lw == 0 && lane < boxes * parts) {
-                            const int box = lane / parts, part = lane - box * parts;
-                            int page, row;
-                            split_page(a.kv, j + box * g.box, page, row);
-                            tma_load_4d(dst + (uint32_t)part * kHalf + (uint32_t)(box * g.box) * 128u,
-                                        kv ? &g.vmap : &g.kmap, 64 * part, row, hk, pg_now, full + st);
-                        }
+                        if (lw == 0)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int it = lane + 32 * y, box = it / parts, part = it - box * parts;
+                                if (it < items)
+                                    tma_load_4d(dst + (uint32_t)part * kHalf + (uint32_t)(box * g.box) * 128u,
+                                                kv ? &g.vmap : &g.kmap, 64 * part, prn[y], hk, pgn[y], full + st);
+                            }
                         continue;
                     }
                     const T* src = static_cast<const T*>(kv ? a.kv.v : a.kv.k) + 8 * ch;

@@ -126,7 +126,7 @@ q4::RaggedArgs ragged(int64_t rows, int64_t n_seqs, const int32_t* start, const 
 }
 
 // Rows of a sequence up to which attn_split_kernel takes it.
-constexpr int kSplitRowsMax = 64;
+constexpr int kSplitRowsMax = 128;
 // Up to this many new tokens of a sequence run token by token.
 constexpr int kLinRecurMax = 8;
 
@@ -367,9 +367,10 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
         g.cnt = cx.attn_cnt;
         g.min_rows = few ? kSplitRowsMax : 0;
         const int dp = kv->head_dim <= 64 ? 64 : 128;
-        // Boxes of a page each (of 128 tokens in larger pages), where pages of
-        // a power of two from 8 on divide a tile or are divided by it.
-        g.box = a.kv.page_shift >= 3 ? std::min((int)kv->page_size, q4::kTaKeys) : 0;
+        // Boxes of the largest power of two of tokens that divides a page, up
+        // to a tile; under 8 they would be more than the 16-byte copies' work.
+        g.box = (int)std::min<int64_t>(kv->page_size & -kv->page_size, q4::kTaKeys);
+        if (g.box < 8) g.box = 0;
         if (g.box && !(page_map(&g.kmap, kv->k, *kv, g.box) && page_map(&g.vmap, kv->v, *kv, g.box))) g.box = 0;
         g.idesc_s = q4::tc_idesc_16(128, q4::kTaKeys, !f16, false);
         g.idesc_o = q4::tc_idesc_16(128, dp, !f16, true);
