@@ -11,7 +11,9 @@ struct CtxView {
     int device, sms;
     bool fail_launch;     // fault injection: launches fail
     int* err;             // device error word
-    float* attn_ws;       // pieces of units that several CTAs share, and their counts
+    float* attn_ws;       // pieces of units that several CTAs share, and their counts;
+                          // the segments' states of the linear attention
+    size_t attn_ws_bytes;
     int* attn_cnt;
 };
 

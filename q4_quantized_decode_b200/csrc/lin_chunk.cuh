@@ -4,9 +4,19 @@
 //   S'  = e^{b_C} S + sum_j e^{b_C - b_j} k_j v_j^T,
 // so a chunk is four matrix products.  They are taken transposed, O^T = S^T Q^T
 // + V^T A^T and S'^T = V^T K', because then a warp's accumulators of S^T (its
-// 16 or 32 value columns as rows, all of k_dim as columns) are, register for
+// 16 value columns as rows, all of k_dim as columns) are, register for
 // register, the A operand of the next chunk's first product: the state never
-// leaves the registers from the sequence's first token to its last.
+// leaves the registers from a segment's first token to its last.
+//
+// Where sequences and heads alone leave SMs idle, sequences are cut into equal
+// segments: a first kernel takes what each segment adds to a state of zero (the
+// last product alone), a second one runs through the segments of every head and
+// leaves each its first state, the third computes all segments' outputs at once.
+//
+// A CTA has a warp for every 16 value columns and one more, which sums the next
+// chunk's decays meanwhile; the next chunk's rows are copied while this one's
+// products run, and each thread looks over the magnitudes of what it copied
+// itself, so a chunk has two barriers (three with conversions).
 //
 // Number formats.  The state and all sums are in 32 bits.  Products run in
 // binary16 (bfloat16 inputs are converted, exactly up to values 2^28 under the
@@ -16,8 +26,8 @@
 // operand of the output products are rounded to binary16 once, because the
 // output is rounded to 16 bits itself.  Powers of two, taken from the chunk's
 // largest magnitudes and the state rows', keep all of that inside binary16's
-// range.  Sums of log decays are in 64 bits (differences of far-apart sums).
-// (The state's unit is at most 2^40, so states up to 2^87 fit.)
+// range (the state's unit is at most 2^40, so states up to 2^87 fit).  Sums of
+// log decays are in 64 bits (differences of far-apart sums).
 // A chunk with infinities, NaN or magnitudes from 2^30 on is run token by token
 // on the same registers instead, where a zero weight touches nothing.
 #pragma once
@@ -28,17 +38,47 @@
 namespace q4 {
 
 constexpr int kLcTokens = 64;
-constexpr int kLcWarps = 4;
-constexpr int kLcThreads = 32 * kLcWarps;
 
-// Value columns of a CTA: 16 MT for each warp.
-__host__ __device__ constexpr int lc_cols(int mt) { return 16 * mt * kLcWarps; }
-__host__ __device__ constexpr int lc_qbytes(int dk, int mt) {        // Q, later the chunk's outputs
-    return kLcTokens * 2 * (dk > lc_cols(mt) ? dk : lc_cols(mt));
+// A CTA's value columns (16 for each of nw warps) and its shared memory: two
+// buffers of Q (later the chunk's outputs), K and V, the split keys, the scores.
+__host__ __device__ constexpr int lc_cols(int nw) { return 16 * nw; }
+__host__ __device__ constexpr int lc_qbytes(int dk, int nw, bool out) {
+    return !out ? 0 : kLcTokens * 2 * (dk > lc_cols(nw) ? dk : lc_cols(nw));
 }
-__host__ __device__ constexpr int lc_smem(int dk, int mt) {
-    return lc_qbytes(dk, mt) + 3 * kLcTokens * dk * 2 + kLcTokens * lc_cols(mt) * 2 + kLcTokens * kLcTokens * 2 +
-           (4 * kLcTokens + 32) * 4;
+__host__ __device__ constexpr int lc_buf(int dk, int nw, bool out) {
+    return lc_qbytes(dk, nw, out) + kLcTokens * 2 * (dk + lc_cols(nw));
+}
+constexpr int kLcDecay = 4 * kLcTokens + 4;          // floats of a chunk's decays
+__host__ __device__ constexpr int lc_smem(int dk, int nw, bool out) {
+    return 2 * lc_buf(dk, nw, out) + 2 * kLcTokens * dk * 2 + (out ? kLcTokens * kLcTokens * 2 : 0) +
+           (2 * kLcDecay + 2 * 3 * 8) * 4;
+}
+
+// The segments of a prompt: `segs` for every sequence, their states and decays.
+struct LinSegArgs {
+    LinArgs a;
+    int segs;
+    float* ws;           // [n_seqs][v_heads][segs][k_dim][v_dim], then [n_seqs][v_heads][segs] decays
+};
+__device__ __forceinline__ float* seg_state(const LinSegArgs& g, int s, int h, int i) {
+    return g.ws + (((int64_t)s * g.a.v_heads + h) * g.segs + i) * g.a.k_dim * g.a.v_dim;
+}
+__device__ __forceinline__ float* seg_decay(const LinSegArgs& g, int s, int h, int i) {
+    return g.ws + (int64_t)g.a.n_seqs * g.a.v_heads * g.segs * g.a.k_dim * g.a.v_dim +
+           ((int64_t)s * g.a.v_heads + h) * g.segs + i;
+}
+// Tokens [t0, t1) of segment i of sequence s (whole chunks; later ones may be
+// empty), and whether it is the last with tokens (or the first of none).
+__device__ __forceinline__ void segment(const LinSegArgs& g, int s, int i, int64_t& t0, int64_t& t1, bool& last) {
+    int64_t lo = g.a.start[s], hi = g.a.start[s + 1];
+    if (lo < 0) lo = 0;
+    if (hi > g.a.rows) hi = g.a.rows;
+    if (hi < lo) hi = lo;
+    const int64_t chunks = (hi - lo + kLcTokens - 1) / kLcTokens;
+    const int64_t len = (chunks + g.segs - 1) / g.segs * kLcTokens;
+    t0 = lo + i * len < hi ? lo + i * len : hi;
+    t1 = lo + (i + 1) * len < hi ? lo + (i + 1) * len : hi;
+    last = t1 == hi && (t0 < t1 || i == 0);
 }
 
 __device__ __forceinline__ float exp2i(int e) {      // 2^e; 0 under and 2^127 over the range
@@ -51,8 +91,11 @@ __device__ __forceinline__ int to_2_14(float x, int cap) {
     return min(cap, 14 - ((__float_as_int(x) >> 23) - 127));
 }
 
-__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {   // a: running, b: two 16-bit floats
-    return __vmaxu2(a, b & 0x7FFF7FFFu);
+__device__ __forceinline__ uint32_t max_abs8(uint32_t m, uint4 v) {      // of 16-bit floats, in halves
+    m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
+    return __vmaxu2(m, v.w & 0x7FFF7FFFu);
 }
 
 // Two 16-bit values times a power of two, as binary16.
@@ -62,215 +105,255 @@ __device__ __forceinline__ uint32_t to_half2(uint32_t v, float pw) {
     return Elem<__half>::pack(f.x * pw, f.y * pw);
 }
 
-template <typename T, int DK, int MT>
-__global__ void __launch_bounds__(kLcThreads, DK * MT <= 256 && DK <= 128 ? 2 : 1) lin_chunk_kernel(const LinArgs a) {
+// Sums of a chunk's log decays by one warp, two tokens a lane: [64] b_i high
+// parts, [64] low parts, [64] e^{b_i}, [64] e^{b_C - b_i}, e^{b_C}, b_C.  Under
+// -104 a decay is zero in 32 bits; padding tokens do not decay.
+__device__ __forceinline__ void chunk_decays(const float* g, int64_t stride, int64_t t, int n, float* out) {
+    const int lane = threadIdx.x & 31;
+    double b0 = 0, b1 = 0;
+    if (2 * lane < n) b0 = g[(t + 2 * lane) * stride];
+    if (2 * lane + 1 < n) b1 = g[(t + 2 * lane + 1) * stride];
+    if (b0 < -104.0) b0 = -104.0;
+    if (b1 < -104.0) b1 = -104.0;
+    b1 += b0;
+    double p = b1;
+    for (int d = 1; d < 32; d <<= 1) {
+        const double y = __shfl_up_sync(0xFFFFFFFFu, p, d);
+        if (lane >= d) p += y;
+    }
+    const double before = p - b1;
+    b0 += before;
+    b1 += before;
+    const double all = __shfl_sync(0xFFFFFFFFu, p, 31);
+    const int i = 2 * lane;
+    *reinterpret_cast<float2*>(out + i) = make_float2((float)b0, (float)b1);
+    *reinterpret_cast<float2*>(out + kLcTokens + i) = make_float2((float)(b0 - (float)b0), (float)(b1 - (float)b1));
+    *reinterpret_cast<float2*>(out + 2 * kLcTokens + i) = make_float2(expf((float)b0), expf((float)b1));
+    *reinterpret_cast<float2*>(out + 3 * kLcTokens + i) = make_float2(expf((float)(all - b0)), expf((float)(all - b1)));
+    if (lane == 0) {
+        out[4 * kLcTokens] = expf((float)all);
+        out[4 * kLcTokens + 1] = (float)all;
+    }
+}
+
+// OUT: a segment's outputs and last state from its first one; else what it adds
+// to a state of zero, and its decay.
+template <typename T, int DK, int NW, bool OUT>
+__global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSegArgs g) {
     constexpr bool kConvert = Elem<T>::kExpMask != Elem<__half>::kExpMask;   // bfloat16 inputs
     constexpr int C = kLcTokens;
-    constexpr int DVS = lc_cols(MT);
+    constexpr int NT = 32 * NW;                          // threads of the products
+    constexpr int DVS = lc_cols(NW);
     constexpr int KB = DK * 2, VB = DVS * 2;             // row bytes
     constexpr int NK = DK / 8;                           // 8-column tiles of the state
+    constexpr uint32_t BUF = lc_buf(DK, NW, OUT);
+    constexpr int KCH = C * (DK / 8), VCH = C * (DVS / 8);   // 16-byte chunks of K (or Q) and V
     extern __shared__ __align__(128) uint8_t lc_raw[];
-    const uint32_t sQ = smem_addr(lc_raw);
-    const uint32_t sK = sQ + lc_qbytes(DK, MT), sHi = sK + C * KB, sLo = sHi + C * KB, sV = sLo + C * KB,
-                   sA = sV + C * VB;
-    float* fl = reinterpret_cast<float*>(lc_raw + lc_smem(DK, MT) - (4 * C + 32) * 4);
-    float* sBh = fl;              // b_i, high and low parts
-    float* sBl = fl + C;
-    float* sEb = fl + 2 * C;      // e^{b_i}
-    float* sW = fl + 3 * C;       // e^{b_C - b_i}
-    volatile float* sMisc = fl + 4 * C;                  // [0] e^{b_C}
-    uint32_t* sMax = reinterpret_cast<uint32_t*>(fl + 4 * C + 4);   // [warp][3] largest |q|, |k|, |v|
+    const LinArgs& a = g.a;
+    const uint32_t base = smem_addr(lc_raw);
+    const uint32_t sHi = base + 2 * BUF, sLo = sHi + C * KB, sA = sLo + C * KB;
+    float* fl = reinterpret_cast<float*>(lc_raw + lc_smem(DK, NW, OUT) - (2 * kLcDecay + 48) * 4);
+    uint32_t* sMax = reinterpret_cast<uint32_t*>(fl + 2 * kLcDecay);   // [2][warp][3] largest |q|, |k|, |v|
 
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, cc = lane & 3;
-    const int h = blockIdx.x, c0 = blockIdx.y * DVS, s = blockIdx.z;
+    const int h = blockIdx.x, c0 = blockIdx.y * DVS;
+    const int s = blockIdx.z / g.segs, seg = blockIdx.z - s * g.segs;
     const int slot = a.slots ? a.slots[s] : s;
     if ((unsigned)slot >= (unsigned)a.n_slots) {
         if (threadIdx.x == 0) set_device_error(a.err, kDevIndex);
         return;
     }
-    int64_t t0 = a.start[s], t1 = a.start[s + 1];
-    if (t0 < 0) t0 = 0;
-    if (t1 > a.rows) t1 = a.rows;
+    int64_t t0, t1;
+    bool last;
+    segment(g, s, seg, t0, t1, last);
+    if (OUT ? t0 == t1 && !last : last || t0 == t1) return;
 
     const T* qb = static_cast<const T*>(a.q) + (int64_t)(h / a.each) * a.k_dim;
     const T* kb = static_cast<const T*>(a.k) + (int64_t)(h / a.each) * a.k_dim;
     const T* vb = static_cast<const T*>(a.v) + (int64_t)h * a.v_dim + c0;
     T* ob = static_cast<T*>(a.out) + (int64_t)h * a.v_dim + c0;
     const float* gb = a.g + h;
-
-    // The state: row warp * 16 MT + 16 mt + gr (+ 8) of its transpose, columns
-    // 8 nk + 2 cc (+ 1).
-    float S[MT][NK][4];
     const int64_t so = ((int64_t)slot * a.v_heads + h) * a.k_dim * a.v_dim;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nk = 0; nk < NK; ++nk)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int dv = c0 + (warp * MT + mt) * 16 + gr + 8 * (x >> 1), dk = 8 * nk + 2 * cc + (x & 1);
-                S[mt][nk][x] = a.state_in && dv < a.v_dim && dk < a.k_dim
-                                   ? a.state_in[so + (int64_t)dk * a.v_dim + dv] : 0.f;
-            }
-    int E = 0;                                           // S holds the state times 2^E
 
-    for (int64_t t = t0; t < t1; t += C) {
-        const int n = (int)(t1 - t < C ? t1 - t : C);
-        for (int x = threadIdx.x; x < C * (DK / 8); x += kLcThreads) {
+    if (warp == NW) {
+        // ---- decays, a chunk ahead ----
+        double sum = 0;
+        chunk_decays(gb, a.g_stride, t0, (int)min((int64_t)C, t1 - t0), fl);
+        __syncthreads();
+        int par = 0;
+        for (int64_t t = t0; t < t1; t += C, par ^= 1) {
+            __syncwarp();
+            sum += fl[par * kLcDecay + 4 * C + 1];
+            if (t + C < t1)
+                chunk_decays(gb, a.g_stride, t + C, (int)min((int64_t)C, t1 - t - C), fl + (par ^ 1) * kLcDecay);
+            __syncthreads();
+        }
+        if (!OUT && lane == 0 && blockIdx.y == 0) *seg_decay(g, s, h, seg) = expf((float)sum);
+        return;
+    }
+
+    // The state: row warp * 16 + gr (+ 8) of its transpose, columns 8 nk + 2 cc
+    // (+ 1); S holds it times 2^E.
+    float S[NK][4];
+    int E = 0;
+    const float* from = !OUT ? nullptr : g.segs > 1 ? seg_state(g, s, h, seg) : a.state_in ? a.state_in + so : nullptr;
+#pragma unroll
+    for (int nk = 0; nk < NK; ++nk)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int dv = c0 + warp * 16 + gr + 8 * (x >> 1), dk = 8 * nk + 2 * cc + (x & 1);
+            S[nk][x] = from && dv < a.v_dim && dk < a.k_dim ? from[(int64_t)dk * a.v_dim + dv] : 0.f;
+        }
+
+    const int tid = threadIdx.x;
+    auto copy = [&](int64_t t, uint32_t buf) {
+        const int n = (int)min((int64_t)C, t1 - t);
+        const uint32_t sQ = buf, sK = buf + lc_qbytes(DK, NW, OUT), sV = sK + C * KB;
+#pragma unroll 4
+        for (int x = tid; x < KCH; x += NT) {
             const int r = x / (DK / 8), ch = x % (DK / 8);
             const bool in = r < n && 8 * ch < a.k_dim;
             const uint32_t dst = (uint32_t)(r * KB + ((ch ^ (r & 7)) << 4));
-            cp_async16(sQ + dst, in ? qb + (t + r) * a.q_stride + 8 * ch : qb, in);
+            if (OUT) cp_async16(sQ + dst, in ? qb + (t + r) * a.q_stride + 8 * ch : qb, in);
             cp_async16(sK + dst, in ? kb + (t + r) * a.k_stride + 8 * ch : kb, in);
         }
-        for (int x = threadIdx.x; x < C * (DVS / 8); x += kLcThreads) {
+#pragma unroll 4
+        for (int x = tid; x < VCH; x += NT) {
             const int r = x / (DVS / 8), ch = x % (DVS / 8);
             const bool in = r < n && c0 + 8 * ch < a.v_dim;
             cp_async16(sV + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4)), in ? vb + (t + r) * a.v_stride + 8 * ch : vb, in);
         }
         cp_async_commit();
-        if (warp == 0) {
-            // Sums of the log decays, two tokens a lane.  Under -104 a decay
-            // is zero in 32 bits; padding tokens do not decay.
-            double b0 = 0, b1 = 0;
-            if (2 * lane < n) b0 = gb[(t + 2 * lane) * a.g_stride];
-            if (2 * lane + 1 < n) b1 = gb[(t + 2 * lane + 1) * a.g_stride];
-            if (b0 < -104.0) b0 = -104.0;
-            if (b1 < -104.0) b1 = -104.0;
-            b1 += b0;
-            double p = b1;
-            for (int d = 1; d < 32; d <<= 1) {
-                const double y = __shfl_up_sync(0xFFFFFFFFu, p, d);
-                if (lane >= d) p += y;
-            }
-            const double before = p - b1;                // exact enough: sums of 32-bit values in 64 bits
-            b0 += before;
-            b1 += before;
-            const double all = __shfl_sync(0xFFFFFFFFu, p, 31);
-            sBh[2 * lane] = (float)b0;
-            sBh[2 * lane + 1] = (float)b1;
-            sBl[2 * lane] = (float)(b0 - (float)b0);
-            sBl[2 * lane + 1] = (float)(b1 - (float)b1);
-            sEb[2 * lane] = expf((float)b0);
-            sEb[2 * lane + 1] = expf((float)b1);
-            sW[2 * lane] = expf((float)(all - b0));
-            sW[2 * lane + 1] = expf((float)(all - b1));
-            if (lane == 0) sMisc[0] = expf((float)all);
-        }
+    };
+    // Waits for this thread's copies and looks over them.
+    auto arrived = [&](uint32_t buf, uint32_t* mx) {
         cp_async_wait<0>();
-        __syncthreads();
-
-        // Largest magnitudes of the chunk.
-        {
-            uint32_t mq = 0, mk = 0, mv = 0;
-            for (int x = threadIdx.x; x < C * (DK / 8); x += kLcThreads) {
-                const uint4 q = lds128(sQ + 16u * x), k = lds128(sK + 16u * x);
-                mq = max_abs2(max_abs2(max_abs2(max_abs2(mq, q.x), q.y), q.z), q.w);
-                mk = max_abs2(max_abs2(max_abs2(max_abs2(mk, k.x), k.y), k.z), k.w);
-            }
-            for (int x = threadIdx.x; x < C * (DVS / 8); x += kLcThreads) {
-                const uint4 v = lds128(sV + 16u * x);
-                mv = max_abs2(max_abs2(max_abs2(max_abs2(mv, v.x), v.y), v.z), v.w);
-            }
-            for (int x = 16; x; x >>= 1) {
-                mq = __vmaxu2(mq, __shfl_xor_sync(0xFFFFFFFFu, mq, x));
-                mk = __vmaxu2(mk, __shfl_xor_sync(0xFFFFFFFFu, mk, x));
-                mv = __vmaxu2(mv, __shfl_xor_sync(0xFFFFFFFFu, mv, x));
-            }
-            if (lane == 0) {
-                sMax[3 * warp] = mq;
-                sMax[3 * warp + 1] = mk;
-                sMax[3 * warp + 2] = mv;
-            }
+        const uint32_t sQ = buf, sK = buf + lc_qbytes(DK, NW, OUT), sV = sK + C * KB;
+        uint32_t m[3] = {0, 0, 0};
+#pragma unroll 4
+        for (int x = tid; x < KCH; x += NT) {
+            const int r = x / (DK / 8), ch = x % (DK / 8);
+            const uint32_t at = (uint32_t)(r * KB + ((ch ^ (r & 7)) << 4));
+            if (OUT) m[0] = max_abs8(m[0], lds128(sQ + at));
+            m[1] = max_abs8(m[1], lds128(sK + at));
         }
-        __syncthreads();
+#pragma unroll 4
+        for (int x = tid; x < VCH; x += NT) {
+            const int r = x / (DVS / 8), ch = x % (DVS / 8);
+            m[2] = max_abs8(m[2], lds128(sV + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4))));
+        }
+#pragma unroll
+        for (int y = 0; y < 3; ++y) {
+            for (int x = 16; x; x >>= 1) m[y] = __vmaxu2(m[y], __shfl_xor_sync(0xFFFFFFFFu, m[y], x));
+            if (lane == 0) mx[3 * warp + y] = m[y];
+        }
+    };
+    auto bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
+
+    if (t0 < t1) {
+        copy(t0, base);
+        arrived(base, sMax);
+    }
+    __syncthreads();
+    int par = 0;
+    for (int64_t t = t0; t < t1; t += C, par ^= 1) {
+        const int n = (int)min((int64_t)C, t1 - t);
+        const uint32_t sQ = base + par * BUF, sK = sQ + lc_qbytes(DK, NW, OUT), sV = sK + C * KB;
+        const float* dec = fl + par * kLcDecay;
+        const float *sBh = dec, *sBl = dec + C, *sEb = dec + 2 * C, *sW = dec + 3 * C;
+        if (t + C < t1) copy(t + C, base + (par ^ 1) * BUF);
+
         float big[3];
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
-            uint32_t m = sMax[x];
+            uint32_t m = sMax[24 * par + x];
 #pragma unroll
-            for (int y = 1; y < kLcWarps; ++y) m = __vmaxu2(m, sMax[3 * y + x]);
+            for (int y = 1; y < NW; ++y) m = __vmaxu2(m, sMax[24 * par + 3 * y + x]);
             const float2 f = Elem<T>::unpack(m);
             big[x] = fmaxf(f.x, f.y);
             if (!(f.x < 1073741824.f && f.y < 1073741824.f)) big[x] = INFINITY;        // NaN too
         }
-        const float decay = sMisc[0];
+        const float decay = dec[4 * C];
         if (!(big[0] < INFINITY && big[1] < INFINITY && big[2] < INFINITY)) {
             // Token by token.
             const float un = exp2i(-E);
             E = 0;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nk = 0; nk < NK; ++nk)
 #pragma unroll
-                for (int nk = 0; nk < NK; ++nk)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) S[mt][nk][x] *= un;
+                for (int x = 0; x < 4; ++x) S[nk][x] *= un;
             for (int r = 0; r < n; ++r) {
                 const float d = expf(gb[(t + r) * a.g_stride]);
-                float v[MT][2], o[MT][2];
+                float v[2], o[2] = {0.f, 0.f};
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int col = (warp * MT + mt) * 16 + gr + 8 * y;
-                        uint32_t u;
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u)
-                                     : "r"(sV + (uint32_t)(r * VB + (((col >> 3) ^ (r & 7)) << 4) + ((col & 6) << 1))));
-                        const float2 f = Elem<T>::unpack(u);
-                        v[mt][y] = col & 1 ? f.y : f.x;
-                        o[mt][y] = 0.f;
-                    }
+                for (int y = 0; y < 2; ++y) {
+                    const int c = warp * 16 + gr + 8 * y;
+                    uint32_t u;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u)
+                                 : "r"(sV + (uint32_t)(r * VB + (((c >> 3) ^ (r & 7)) << 4) + ((c & 6) << 1))));
+                    const float2 f = Elem<T>::unpack(u);
+                    v[y] = c & 1 ? f.y : f.x;
+                }
 #pragma unroll
                 for (int nk = 0; nk < NK; ++nk) {
-                    uint32_t uq, uk;
                     const uint32_t at = (uint32_t)(r * KB + ((nk ^ (r & 7)) << 4) + 4 * cc);
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(uq) : "r"(sQ + at));
+                    uint32_t uq = 0, uk;
+                    if (OUT) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(uq) : "r"(sQ + at));
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(uk) : "r"(sK + at));
                     const float2 q = Elem<T>::unpack(uq), k = Elem<T>::unpack(uk);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            float& s0 = S[mt][nk][2 * y];
-                            float& s1 = S[mt][nk][2 * y + 1];
-                            s0 = fmaf(s0, d, k.x * v[mt][y]);
-                            s1 = fmaf(s1, d, k.y * v[mt][y]);
-                            if (8 * nk + 2 * cc < a.k_dim) {
-                                o[mt][y] = fmaf(q.x * a.scale, s0, o[mt][y]);
-                                o[mt][y] = fmaf(q.y * a.scale, s1, o[mt][y]);
-                            }
+                    for (int y = 0; y < 2; ++y) {
+                        float& s0 = S[nk][2 * y];
+                        float& s1 = S[nk][2 * y + 1];
+                        s0 = fmaf(s0, d, k.x * v[y]);
+                        s1 = fmaf(s1, d, k.y * v[y]);
+                        if (OUT && 8 * nk + 2 * cc < a.k_dim) {
+                            o[y] = fmaf(q.x * a.scale, s0, o[y]);
+                            o[y] = fmaf(q.y * a.scale, s1, o[y]);
                         }
+                    }
                 }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                if (OUT)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float f = o[mt][y];
+                        float f = o[y];
                         f += __shfl_xor_sync(0xFFFFFFFFu, f, 1);
                         f += __shfl_xor_sync(0xFFFFFFFFu, f, 2);
-                        const int col = (warp * MT + mt) * 16 + gr + 8 * y;
-                        if (cc == 0 && c0 + col < a.v_dim) ob[(t + r) * a.o_stride + col] = Elem<T>::round(f);
+                        const int c = warp * 16 + gr + 8 * y;
+                        if (cc == 0 && c0 + c < a.v_dim) ob[(t + r) * a.o_stride + c] = Elem<T>::round(f);
                     }
             }
-            __syncthreads();
-            continue;
-        }
-
-        // Powers: q, v (and k of the scores) times 2^sq, 2^sv (2^skk) in
-        // binary16, the split keys times 2^sk, the scores times 2^-ta.
-        const int sk = to_2_14(big[1], 24);
-        const int sq = kConvert ? to_2_14(big[0], 24) : 0, sv = kConvert ? to_2_14(big[2], 16) : 0;
-        const int skk = kConvert ? sk : 0;
-        const float bound = (float)DK * (big[0] * exp2i(sq)) * (big[1] * exp2i(skk));   // of a score
-        const int ta = bound == 0.f ? 0 : max(-100, (__float_as_int(bound) >> 23) - 127 - 14);
-        {
+        } else {
+            // Powers: q, v (and k of the scores) times 2^sq, 2^sv (2^skk) in
+            // binary16, the split keys times 2^sk, the scores times 2^-ta.
+            const int sk = to_2_14(big[1], 24);
+            const int sq = kConvert ? to_2_14(big[0], 24) : 0, sv = kConvert ? to_2_14(big[2], 16) : 0;
+            const int skk = kConvert ? sk : 0;
+            const float bound = (float)DK * (big[0] * exp2i(sq)) * (big[1] * exp2i(skk));   // of a score
+            const int ta = bound == 0.f ? 0 : max(-100, (__float_as_int(bound) >> 23) - 127 - 14);
             const float pk = exp2i(sk);
-            for (int x = threadIdx.x; x < C * (DK / 8); x += kLcThreads) {
-                const int r = x / (DK / 8);
+            if (kConvert) {
+                const float pv = exp2i(sv), pq = exp2i(sq);
+                for (int x = tid; x < VCH; x += NT) {
+                    const uint4 v = lds128(sV + 16u * x);
+                    sts128(sV + 16u * x, make_uint4(to_half2<T>(v.x, pv), to_half2<T>(v.y, pv), to_half2<T>(v.z, pv),
+                                                    to_half2<T>(v.w, pv)));
+                }
+                for (int x = tid; x < KCH; x += NT) {
+                    if (OUT) {
+                        const uint4 q = lds128(sQ + 16u * x);
+                        sts128(sQ + 16u * x, make_uint4(to_half2<T>(q.x, pq), to_half2<T>(q.y, pq),
+                                                        to_half2<T>(q.z, pq), to_half2<T>(q.w, pq)));
+                    }
+                }
+            }
+            // The split keys (and, converted, the scores' keys).
+#pragma unroll 4
+            for (int x = tid; x < KCH; x += NT) {
+                const float w = sW[x / (DK / 8)] * pk;
                 const uint4 k = lds128(sK + 16u * x);
-                const float w = sW[r] * pk;
                 const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
                 uint32_t hi[4], lo[4], kk[4];
 #pragma unroll
@@ -284,219 +367,234 @@ __global__ void __launch_bounds__(kLcThreads, DK * MT <= 256 && DK <= 128 ? 2 : 
                 }
                 sts128(sHi + 16u * x, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                 sts128(sLo + 16u * x, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                if (kConvert) {
-                    sts128(sK + 16u * x, make_uint4(kk[0], kk[1], kk[2], kk[3]));
-                    const uint4 q = lds128(sQ + 16u * x);
-                    const float pq = exp2i(sq);
-                    sts128(sQ + 16u * x, make_uint4(to_half2<T>(q.x, pq), to_half2<T>(q.y, pq), to_half2<T>(q.z, pq),
-                                                    to_half2<T>(q.w, pq)));
-                }
+                if (kConvert && OUT) sts128(sK + 16u * x, make_uint4(kk[0], kk[1], kk[2], kk[3]));
             }
-            if (kConvert) {
-                const float pv = exp2i(sv);
-                for (int x = threadIdx.x; x < C * (DVS / 8); x += kLcThreads) {
-                    const uint4 v = lds128(sV + 16u * x);
-                    sts128(sV + 16u * x, make_uint4(to_half2<T>(v.x, pv), to_half2<T>(v.y, pv), to_half2<T>(v.z, pv),
-                                                    to_half2<T>(v.w, pv)));
-                }
-            }
-        }
-        __syncthreads();
+            if (kConvert) bar();
 
-        // Scores of the ten 16 x 16 blocks on and under the diagonal, each
-        // with its decays, as the transposed product's B operand [i][j].
-        for (int blk = warp; blk < 10; blk += kLcWarps) {
-            const int bi = blk == 0 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bj = blk - bi * (bi + 1) / 2;
-            if (16 * bi >= n) continue;
-            float sc[2][4];
+            float O[OUT ? C / 8 : 1][4];
+            if constexpr (OUT) {
+                // Scores of the ten 16 x 16 blocks on and under the diagonal in
+                // halves of eight columns, each with its decays, as the
+                // transposed product's B operand [i][j].
+                for (int hb = warp; hb < 20; hb += NW) {
+                    const int blk = hb >> 1;
+                    const int bi = blk == 0 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bj = blk - bi * (bi + 1) / 2;
+                    if (16 * bi >= n) continue;
+                    float sc[4] = {0.f, 0.f, 0.f, 0.f};
+                    const int jb = 16 * bj + 8 * (hb & 1);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) sc[x >> 2][x & 3] = 0.f;
+                    for (int kk = 0; kk < DK / 16; kk += 2) {
+                        uint32_t af[4], ag[4], bf[4];
+                        const int ra = 16 * bi + (lane & 15), ca = 2 * kk + (lane >> 4);
+                        ldmatrix4(af, sQ + (uint32_t)(ra * KB + ((ca ^ (ra & 7)) << 4)));
+                        ldmatrix4(ag, sQ + (uint32_t)(ra * KB + (((ca + 2) ^ (ra & 7)) << 4)));
+                        const int rb = jb + (lane & 7), cb = 2 * kk + (lane >> 3);
+                        ldmatrix4(bf, sK + (uint32_t)(rb * KB + ((cb ^ (rb & 7)) << 4)));
+                        mma16816<__half>(sc, af, bf[0], bf[1]);
+                        mma16816<__half>(sc, ag, bf[2], bf[3]);
+                    }
+                    const float pa = exp2i(-ta);
 #pragma unroll
-            for (int kk = 0; kk < DK / 16; ++kk) {
-                uint32_t af[4], bf[4];
-                const int ra = 16 * bi + (lane & 15), ca = 2 * kk + (lane >> 4);
-                ldmatrix4(af, sQ + (uint32_t)(ra * KB + ((ca ^ (ra & 7)) << 4)));
-                const int rb = 16 * bj + (lane & 7) + ((lane >> 4) << 3), cb = 2 * kk + ((lane >> 3) & 1);
-                ldmatrix4(bf, sK + (uint32_t)(rb * KB + ((cb ^ (rb & 7)) << 4)));
-                mma16816<__half>(sc[0], af, bf[0], bf[1]);
-                mma16816<__half>(sc[1], af, bf[2], bf[3]);
-            }
-            const float pa = exp2i(-ta);
+                    for (int r = 0; r < 2; ++r) {
+                        const int i = 16 * bi + gr + 8 * r;
+                        const float bh = sBh[i], bl = sBl[i];
+                        float f[2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int i = 16 * bi + gr + 8 * r;
-                const float bh = sBh[i], bl = sBl[i];
+                        for (int x = 0; x < 2; ++x) {
+                            const int j = jb + 2 * cc + x;
+                            f[x] = j <= i ? sc[2 * r + x] * pa * __expf((bh - sBh[j]) + (bl - sBl[j])) : 0.f;
+                        }
+                        const uint32_t at = sA + (uint32_t)(i * (2 * C) + (((jb >> 3) ^ (i & 7)) << 4) + 4 * cc);
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(Elem<__half>::pack(f[0], f[1])) : "memory");
+                    }
+                }
+
+                // O^T = (S^T 2^row) Q^T, then brought to the scores' scale with
+                // the decays e^{b_i}.
+#pragma unroll
+                for (int x = 0; x < C / 8; ++x)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) O[x][y] = 0.f;
+                int rs[2];
+                float rp[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    float f[2];
+                    float m = 0.f;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int j = 16 * bj + 8 * y + 2 * cc + x;
-                        f[x] = j <= i ? sc[y][2 * r + x] * pa * __expf((bh - sBh[j]) + (bl - sBl[j])) : 0.f;
+                    for (int nk = 0; nk < NK; ++nk) m = fmaxf(m, fmaxf(fabsf(S[nk][2 * y]), fabsf(S[nk][2 * y + 1])));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+                    const int e = (__float_as_int(m) >> 23) - 127;
+                    rs[y] = m == 0.f || e > 127 ? 0 : min(126, 14 - e);
+                    rp[y] = exp2i(rs[y]);
+                }
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk) {
+                    uint32_t af[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float* p = S[2 * kk + (x >> 1)];
+                        const float f = rp[x & 1];
+                        af[x] = Elem<__half>::pack(p[2 * (x & 1)] * f, p[2 * (x & 1) + 1] * f);
                     }
-                    const uint32_t at = sA + (uint32_t)(i * (2 * C) + (((2 * bj + y) ^ (i & 7)) << 4) + 4 * cc);
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(Elem<__half>::pack(f[0], f[1])) : "memory");
+#pragma unroll
+                    for (int np = 0; np < C / 16; ++np) {
+                        uint32_t bf[4];
+                        const int rb = 16 * np + (lane & 7) + ((lane >> 4) << 3), cb = 2 * kk + ((lane >> 3) & 1);
+                        ldmatrix4(bf, sQ + (uint32_t)(rb * KB + ((cb ^ (rb & 7)) << 4)));
+                        mma16816<__half>(O[2 * np], af, bf[0], bf[1]);
+                        mma16816<__half>(O[2 * np + 1], af, bf[2], bf[3]);
+                    }
                 }
-            }
-        }
-
-        // O^T = (S^T 2^row) Q^T, then brought to the scores' scale with the
-        // decays e^{b_i}.
-        float O[MT][C / 8][4];
+                float rf[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+                for (int y = 0; y < 2; ++y) rf[y] = exp2i(-rs[y] - E + skk + sv - ta);
 #pragma unroll
-            for (int x = 0; x < C / 8; ++x)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) O[mt][x][y] = 0.f;
-        int rs[MT][2];
-        float rp[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                float m = 0.f;
-#pragma unroll
-                for (int nk = 0; nk < NK; ++nk) m = fmaxf(m, fmaxf(fabsf(S[mt][nk][2 * y]), fabsf(S[mt][nk][2 * y + 1])));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                const int e = (__float_as_int(m) >> 23) - 127;
-                rs[mt][y] = m == 0.f || e > 127 ? 0 : min(126, 14 - e);
-                rp[mt][y] = exp2i(rs[mt][y]);
-            }
-#pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) {
-            uint32_t af[MT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float* p = S[mt][2 * kk + (x >> 1)];
-                    const float f = rp[mt][x & 1];
-                    af[mt][x] = Elem<__half>::pack(p[2 * (x & 1)] * f, p[2 * (x & 1) + 1] * f);
-                }
-#pragma unroll
-            for (int np = 0; np < C / 16; ++np) {
-                uint32_t bf[4];
-                const int rb = 16 * np + (lane & 7) + ((lane >> 4) << 3), cb = 2 * kk + ((lane >> 3) & 1);
-                ldmatrix4(bf, sQ + (uint32_t)(rb * KB + ((cb ^ (rb & 7)) << 4)));
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma16816<__half>(O[mt][2 * np], af[mt], bf[0], bf[1]);
-                    mma16816<__half>(O[mt][2 * np + 1], af[mt], bf[2], bf[3]);
-                }
-            }
-        }
-        const int En = sk + sv;                          // the unit that this chunk's keys and values give
-        {
-            float rf[MT][2];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) rf[mt][y] = exp2i(-rs[mt][y] - E + skk + sv - ta);
-#pragma unroll
-            for (int x = 0; x < C / 8; ++x) {
-                const float2 eb = *reinterpret_cast<const float2*>(sEb + 8 * x + 2 * cc);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int x = 0; x < C / 8; ++x) {
+                    const float2 eb = *reinterpret_cast<const float2*>(sEb + 8 * x + 2 * cc);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        O[mt][x][2 * y] *= rf[mt][y] * eb.x;
-                        O[mt][x][2 * y + 1] *= rf[mt][y] * eb.y;
+                        O[x][2 * y] *= rf[y] * eb.x;
+                        O[x][2 * y + 1] *= rf[y] * eb.y;
                     }
+                }
             }
-            const float f1 = exp2i(En - E);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            {
+                const float f1 = exp2i(sk + sv - E);     // to the unit of this chunk's keys and values
 #pragma unroll
                 for (int nk = 0; nk < NK; ++nk)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) S[mt][nk][x] = S[mt][nk][x] * decay * f1;
-            E = En;
-        }
-        __syncthreads();
+                    for (int x = 0; x < 4; ++x) S[nk][x] = S[nk][x] * decay * f1;
+                E = sk + sv;
+            }
+            bar();
 
-        // O^T += V^T A^T and S^T += V^T K' (both parts), 16 tokens at a time.
+            // O^T += V^T A^T and S^T += V^T K' (both parts), 16 tokens at a time.
 #pragma unroll
-        for (int kt = 0; kt < C / 16; ++kt) {
-            if (16 * kt < n) {
-                uint32_t vf[MT][4];
+            for (int kt = 0; kt < C / 16; ++kt) {
+                if (16 * kt < n) {
+                    uint32_t vf[4];
+                    {
+                        // transposed blocks: value columns 0-7, 8-15 at tokens 0-7, then at 8-15
+                        const int r = 16 * kt + (lane & 7) + ((lane >> 4) << 3);
+                        const int ch = 2 * warp + ((lane >> 3) & 1);
+                        ldmatrix4t(vf, sV + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4)));
+                    }
+                    if constexpr (OUT) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    // transposed blocks: value columns 0-7, 8-15 at tokens 0-7, then at 8-15
-                    const int r = 16 * kt + (lane & 7) + ((lane >> 4) << 3);
-                    const int ch = 2 * (warp * MT + mt) + ((lane >> 3) & 1);
-                    ldmatrix4t(vf[mt], sV + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4)));
-                }
-#pragma unroll
-                for (int np = kt; np < C / 16; ++np) {
-                    uint32_t bf[4];
-                    const int rb = 16 * np + (lane & 7) + ((lane >> 4) << 3), cb = 2 * kt + ((lane >> 3) & 1);
-                    if (16 * np < n) {
-                        ldmatrix4(bf, sA + (uint32_t)(rb * (2 * C) + ((cb ^ (rb & 7)) << 4)));
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            mma16816<__half>(O[mt][2 * np], vf[mt], bf[0], bf[1]);
-                            mma16816<__half>(O[mt][2 * np + 1], vf[mt], bf[2], bf[3]);
+                        for (int np = kt; np < C / 16; ++np) {
+                            const int rb = 16 * np + (lane & 7) + ((lane >> 4) << 3), cb = 2 * kt + ((lane >> 3) & 1);
+                            if (16 * np < n) {
+                                uint32_t bf[4];
+                                ldmatrix4(bf, sA + (uint32_t)(rb * (2 * C) + ((cb ^ (rb & 7)) << 4)));
+                                mma16816<__half>(O[2 * np], vf, bf[0], bf[1]);
+                                mma16816<__half>(O[2 * np + 1], vf, bf[2], bf[3]);
+                            }
                         }
                     }
-                }
 #pragma unroll
-                for (int np = 0; np < DK / 16; ++np) {
-                    uint32_t hf[4], lf[4];
-                    const int r = 16 * kt + (lane & 15), ch = 2 * np + (lane >> 4);
-                    const uint32_t at = (uint32_t)(r * KB + ((ch ^ (r & 7)) << 4));
-                    ldmatrix4t(hf, sHi + at);
-                    ldmatrix4t(lf, sLo + at);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma16816<__half>(S[mt][2 * np], vf[mt], hf[0], hf[1]);
-                        mma16816<__half>(S[mt][2 * np + 1], vf[mt], hf[2], hf[3]);
-                        mma16816<__half>(S[mt][2 * np], vf[mt], lf[0], lf[1]);
-                        mma16816<__half>(S[mt][2 * np + 1], vf[mt], lf[2], lf[3]);
+                    for (int np = 0; np < DK / 16; ++np) {
+                        uint32_t hf[4], lf[4];
+                        const int r = 16 * kt + (lane & 15), ch = 2 * np + (lane >> 4);
+                        const uint32_t at = (uint32_t)(r * KB + ((ch ^ (r & 7)) << 4));
+                        ldmatrix4t(hf, sHi + at);
+                        ldmatrix4t(lf, sLo + at);
+                        mma16816<__half>(S[2 * np], vf, hf[0], hf[1]);
+                        mma16816<__half>(S[2 * np + 1], vf, hf[2], hf[3]);
+                        mma16816<__half>(S[2 * np], vf, lf[0], lf[1]);
+                        mma16816<__half>(S[2 * np + 1], vf, lf[2], lf[3]);
                     }
                 }
             }
-        }
 
-        // Outputs: transposed into the queries' place, then out in rows.
-        const float fo = exp2i(ta - sq - skk - sv) * a.scale;
+            if constexpr (OUT) {
+                // Outputs: transposed into the queries' place, then out in rows.
+                const float fo = exp2i(ta - sq - skk - sv) * a.scale;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+                for (int np = 0; np < C / 16; ++np) {
+                    // blocks: (columns 0-7, tokens 0-7), (columns 8-15, tokens 0-7), the same of tokens 8-15
+                    uint32_t p[4];
 #pragma unroll
-            for (int np = 0; np < C / 16; ++np) {
-                // blocks: (columns 0-7, tokens 0-7), (columns 8-15, tokens 0-7), the same of tokens 8-15
-                uint32_t p[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float* o = O[mt][2 * np + (x >> 1)];
-                    p[x] = Elem<T>::pack(o[2 * (x & 1)] * fo, o[2 * (x & 1) + 1] * fo);
+                    for (int x = 0; x < 4; ++x) {
+                        const float* o = O[2 * np + (x >> 1)];
+                        p[x] = Elem<T>::pack(o[2 * (x & 1)] * fo, o[2 * (x & 1) + 1] * fo);
+                    }
+                    const int r = 16 * np + (lane & 7) + ((lane >> 4) << 3);
+                    const int ch = 2 * warp + ((lane >> 3) & 1);
+                    stmatrix4t(sQ + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4)), p[0], p[1], p[2], p[3]);
                 }
-                const int r = 16 * np + (lane & 7) + ((lane >> 4) << 3);
-                const int ch = 2 * (warp * MT + mt) + ((lane >> 3) & 1);
-                stmatrix4t(sQ + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4)), p[0], p[1], p[2], p[3]);
-            }
-        __syncwarp();
+                __syncwarp();
 #pragma unroll
-        for (int x = 0; x < C * 2 * MT / 32; ++x) {
-            const int r = (x * 32 + lane) / (2 * MT), ch = 2 * warp * MT + lane % (2 * MT);
-            const uint4 v = lds128(sQ + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4)));
-            if (r < n && c0 + 8 * ch < a.v_dim)
-                *reinterpret_cast<uint4*>(ob + (t + r) * a.o_stride + 8 * ch) = v;
+                for (int x = 0; x < C * 2 / 32; ++x) {
+                    const int r = (x * 32 + lane) / 2, ch = 2 * warp + (lane & 1);
+                    const uint4 v = lds128(sQ + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4)));
+                    if (r < n && c0 + 8 * ch < a.v_dim)
+                        *reinterpret_cast<uint4*>(ob + (t + r) * a.o_stride + 8 * ch) = v;
+                }
+            }
         }
+        if (t + C < t1) arrived(base + (par ^ 1) * BUF, sMax + 24 * (par ^ 1));
         __syncthreads();
     }
 
+    float* to = OUT ? (last ? a.state_out + so : nullptr) : seg_state(g, s, h, seg);
+    if (!to) return;
     const float un = exp2i(-E);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nk = 0; nk < NK; ++nk)
 #pragma unroll
-        for (int nk = 0; nk < NK; ++nk)
+        for (int x = 0; x < 4; ++x) {
+            const int dv = c0 + warp * 16 + gr + 8 * (x >> 1), dk = 8 * nk + 2 * cc + (x & 1);
+            if (dv < a.v_dim && dk < a.k_dim) to[(int64_t)dk * a.v_dim + dv] = S[nk][x] * un;
+        }
+}
+
+// The segments' first states: in each place of a segment's gain, the state
+// that it starts from.
+constexpr int kLinScanThreads = 128;
+static __global__ void __launch_bounds__(kLinScanThreads) lin_scan_kernel(const LinSegArgs g) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const LinArgs& a = g.a;
+    const int h = blockIdx.y, s = blockIdx.z;
+    const int slot = a.slots ? a.slots[s] : s;
+    if ((unsigned)slot >= (unsigned)a.n_slots) return;           // reported by the segments' kernel
+    const int64_t e = ((int64_t)blockIdx.x * kLinScanThreads + threadIdx.x) * 4, size = (int64_t)a.k_dim * a.v_dim;
+    if (e >= size) return;
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.state_in) S = *reinterpret_cast<const float4*>(a.state_in + ((int64_t)slot * a.v_heads + h) * size + e);
+    int n = g.segs;                                              // segments that have a gain
+    for (int i = 0; i < g.segs; ++i) {
+        int64_t t0, t1;
+        bool last;
+        segment(g, s, i, t0, t1, last);
+        if (last) {
+            n = i;
+            break;
+        }
+    }
+    float* p = seg_state(g, s, h, 0) + e;
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+        float4 d[kAhead];
+        float w[kAhead];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int dv = c0 + (warp * MT + mt) * 16 + gr + 8 * (x >> 1), dk = 8 * nk + 2 * cc + (x & 1);
-                if (dv < a.v_dim && dk < a.k_dim) a.state_out[so + (int64_t)dk * a.v_dim + dv] = S[mt][nk][x] * un;
+        for (int y = 0; y < kAhead; ++y)
+            if (i0 + y < n) {
+                d[y] = *reinterpret_cast<const float4*>(p + (i0 + y) * size);
+                w[y] = *seg_decay(g, s, h, i0 + y);
             }
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y)
+            if (i0 + y < n) {
+                *reinterpret_cast<float4*>(p + (i0 + y) * size) = S;
+                S.x = fmaf(S.x, w[y], d[y].x);
+                S.y = fmaf(S.y, w[y], d[y].y);
+                S.z = fmaf(S.z, w[y], d[y].z);
+                S.w = fmaf(S.w, w[y], d[y].w);
+            }
+    }
+    if (n < g.segs) *reinterpret_cast<float4*>(p + n * size) = S;
 }
 
 }  // namespace q4

@@ -129,6 +129,8 @@ q4::RaggedArgs ragged(int64_t rows, int64_t n_seqs, const int32_t* start, const 
 constexpr int kSplitRowsMax = 128;
 // Up to this many new tokens of a sequence run token by token.
 constexpr int kLinRecurMax = 8;
+// Chunks of a prompt's segment, at least.
+constexpr int kLinSegChunks = 4;
 
 int split_dp(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
@@ -187,17 +189,19 @@ cudaError_t tc_setup() {
     return cudaFuncSetAttribute(q4::attn_tc_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, q4::ta_smem(DP));
 }
 
-template <typename T, int DK, int MT>
+template <typename T, int DK, int NW>
 cudaError_t chunk_setup() {
-    return cudaFuncSetAttribute(q4::lin_chunk_kernel<T, DK, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                q4::lc_smem(DK, MT));
+    const cudaError_t e = cudaFuncSetAttribute(q4::lin_chunk_kernel<T, DK, NW, true>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, q4::lc_smem(DK, NW, true));
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(q4::lin_chunk_kernel<T, DK, NW, false>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       q4::lc_smem(DK, NW, false));
 }
 template <typename T>
 cudaError_t setup_type() {
     for (cudaError_t e : {split_setup<T, 64>(), split_setup<T, 128>(), split_setup<T, 256>(), tc_setup<T, 64>(),
-                          tc_setup<T, 128>(), chunk_setup<T, 64, 1>(),
-                          chunk_setup<T, 64, 2>(), chunk_setup<T, 128, 1>(), chunk_setup<T, 128, 2>(),
-                          chunk_setup<T, 256, 1>()})
+                          tc_setup<T, 128>(), chunk_setup<T, 64, 4>(), chunk_setup<T, 64, 8>(),
+                          chunk_setup<T, 128, 4>(), chunk_setup<T, 128, 8>(), chunk_setup<T, 256, 4>()})
         if (e != cudaSuccess) return e;
     return cudaSuccess;
 }
@@ -397,21 +401,46 @@ cudaError_t lin_recur_launch(const q4::LinArgs& a, cudaStream_t st) {
     return launch(q4::lin_recur_kernel<T, 16>, grid, q4::kLinThreads, 0, st, a);
 }
 
-template <typename T, int DK, int MT>
-cudaError_t lin_chunk_launch(const q4::LinArgs& a, cudaStream_t st) {
-    const dim3 grid((unsigned)a.v_heads, (unsigned)((a.v_dim + q4::lc_cols(MT) - 1) / q4::lc_cols(MT)),
-                    (unsigned)a.n_seqs);
-    return launch(q4::lin_chunk_kernel<T, DK, MT>, grid, q4::kLcThreads, q4::lc_smem(DK, MT), st, a);
+template <typename T, int DK, int NW, bool OUT>
+cudaError_t lin_chunk_launch(const q4::LinSegArgs& g, cudaStream_t st) {
+    const dim3 grid((unsigned)g.a.v_heads, (unsigned)((g.a.v_dim + q4::lc_cols(NW) - 1) / q4::lc_cols(NW)),
+                    (unsigned)(g.a.n_seqs * g.segs));
+    return launch(q4::lin_chunk_kernel<T, DK, NW, OUT>, grid, 32 * (NW + 1), q4::lc_smem(DK, NW, OUT), st, g);
+}
+template <typename T, bool OUT>
+cudaError_t lin_chunks(const q4::LinSegArgs& g, cudaStream_t st) {
+    const bool wide = g.a.v_dim > 64;
+    if (g.a.k_dim <= 64) return wide ? lin_chunk_launch<T, 64, 8, OUT>(g, st) : lin_chunk_launch<T, 64, 4, OUT>(g, st);
+    if (g.a.k_dim <= 128) return wide ? lin_chunk_launch<T, 128, 8, OUT>(g, st) : lin_chunk_launch<T, 128, 4, OUT>(g, st);
+    return lin_chunk_launch<T, 256, 4, OUT>(g, st);
 }
 
-// Prompts run in chunks; a warp takes 32 value columns (half the shared-memory
-// reads of a product) where that leaves two CTAs for every SM, 16 otherwise.
+// Prompts run in chunks, cut into segments where sequences and heads alone
+// would leave SMs idle (a segment costs half as much again: its gain is
+// computed first).
 template <typename T>
-cudaError_t lin_prompt_launch(const q4::LinArgs& a, int sms, cudaStream_t st) {
-    const bool wide = a.v_dim > 64 && (int64_t)a.n_seqs * a.v_heads * ((a.v_dim + 127) / 128) >= 2 * (int64_t)sms;
-    if (a.k_dim <= 64) return wide ? lin_chunk_launch<T, 64, 2>(a, st) : lin_chunk_launch<T, 64, 1>(a, st);
-    if (a.k_dim <= 128) return wide ? lin_chunk_launch<T, 128, 2>(a, st) : lin_chunk_launch<T, 128, 1>(a, st);
-    return lin_chunk_launch<T, 256, 1>(a, st);
+cudaError_t lin_prompt_launch(const q4::LinArgs& a, int64_t max_new, const q4::CtxView& cx, cudaStream_t st) {
+    q4::LinSegArgs g;
+    g.a = a;
+    g.ws = cx.attn_ws;
+    const int64_t slices = a.k_dim > 128 || a.v_dim <= 64 ? (a.v_dim + 63) / 64 : (a.v_dim + 127) / 128;
+    const int64_t ctas = (int64_t)a.n_seqs * a.v_heads * slices;
+    const int64_t chunks = (std::min(max_new, a.rows) + q4::kLcTokens - 1) / q4::kLcTokens;
+    const int64_t room = (int64_t)(cx.attn_ws_bytes / sizeof(float)) /
+                         ((int64_t)a.n_seqs * a.v_heads * ((int64_t)a.k_dim * a.v_dim + 1));
+    int64_t segs = std::min<int64_t>({cx.sms / ctas, chunks / kLinSegChunks, room, 65535 / a.n_seqs});
+    g.segs = (int)std::max<int64_t>(segs, 1);
+    if (g.segs < 3) g.segs = 1;
+    if (g.segs > 1) {
+        cudaError_t e = lin_chunks<T, false>(g, st);
+        if (e != cudaSuccess) return e;
+        const int64_t size = (int64_t)a.k_dim * a.v_dim;
+        e = launch(q4::lin_scan_kernel, dim3((unsigned)((size / 4 + q4::kLinScanThreads - 1) / q4::kLinScanThreads),
+                                             (unsigned)a.v_heads, (unsigned)a.n_seqs),
+                   q4::kLinScanThreads, 0, st, g);
+        if (e != cudaSuccess) return e;
+    }
+    return lin_chunks<T, true>(g, st);
 }
 
 }  // namespace
@@ -477,6 +506,6 @@ extern "C" int q4gemv_linattn(q4gemv_t h, const q4gemv_linattn_args* args, int64
     const bool f16 = p.dtype == Q4GEMV_F16;
     if (max_new <= kLinRecurMax)
         return launch_status(h, f16 ? lin_recur_launch<__half>(a, st) : lin_recur_launch<__nv_bfloat16>(a, st), call);
-    return launch_status(h, f16 ? lin_prompt_launch<__half>(a, cx.sms, st)
-                                : lin_prompt_launch<__nv_bfloat16>(a, cx.sms, st), call);
+    return launch_status(h, f16 ? lin_prompt_launch<__half>(a, max_new, cx, st)
+                                : lin_prompt_launch<__nv_bfloat16>(a, max_new, cx, st), call);
 }

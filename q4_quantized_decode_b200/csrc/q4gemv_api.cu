@@ -128,6 +128,7 @@ struct q4gemv_ctx {
     __half* hio = nullptr;           // device copies of host x_in / x_out of run_stack
     float* attn_ws = nullptr;        // shared pieces of the paged attention, and their counts
     int* attn_cnt = nullptr;
+    size_t attn_ws_bytes = 0;
     uint8_t* ximg = nullptr;         // activation image of the tensor-core GEMM
     size_t ximg_bytes = 0;
     int64_t hio_elems = 0;           // per vector
@@ -798,6 +799,7 @@ int q4gemv_create(q4gemv_t* out, int device) {
             h->yacc_floats = kYaccPrealloc;
             h->ximg_bytes = kXimgPrealloc;
             h->cnt_elems = kMaxTiles;
+            h->attn_ws_bytes = attn_ws_bytes;
         }
         const char* mode = getenv("Q4GEMV_STACK_MODE");
         if (mode && !strcmp(mode, "kernels")) h->stack_mode = kStackKernels;
@@ -1678,6 +1680,7 @@ q4::CtxView q4::ctx_view(q4gemv_t h) {
     v.err = h->err;
     v.attn_ws = h->attn_ws;
     v.attn_cnt = h->attn_cnt;
+    v.attn_ws_bytes = h->attn_ws_bytes;
     return v;
 }
 
