@@ -14,7 +14,8 @@ SOURCES = ["q4gemv_api.cu", "q4gemv_noalloc.cu", "mix_api.cu"]
 HEADERS = ["device_common.cuh", "partition.cuh", "gemv_dp2a.cuh", "gemv_mma.cuh", "stack.cuh",
            "gemm_tc.cuh", "gemv_swiglu.cuh", "gemv_tcs.cuh", "ctx_view.h", "mix_common.cuh",
            "kv_append.cuh", "attn_rows.cuh", "attn_split.cuh", "mma_common.cuh",
-           "lin_chunk.cuh", "attn_tc.cuh", "tc_common.cuh", "linattn.cuh"]
+           "lin_chunk.cuh", "attn_tc.cuh", "tc_common.cuh", "lin_seg.cuh",
+           "lin_tc.cuh", "linattn.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

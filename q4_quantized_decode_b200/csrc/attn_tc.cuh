@@ -329,30 +329,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
                  : "memory");
 }
 
-// A wait that gives up when another role has, or after about 20 seconds (the
-// longest that a role keeps others waiting in earnest is a unit taken row by
-// row, milliseconds for ordinary contexts).
-__device__ __forceinline__ bool ta_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (uint32_t i = 0;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 15) == 15 && (*abort_flag || clock64() - t0 > (1ll << 35))) return false;
-    }
-}
-
-__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-// The same; whether `ok` holds for all of them.
-__device__ __forceinline__ bool all_softmax(bool ok) {
-    uint32_t all;
-    asm volatile("{\n\t.reg .pred p, q;\n\t"
-                 "setp.ne.u32 p, %1, 0;\n\t"
-                 "barrier.cta.red.and.pred q, 1, 256, p;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(all) : "r"((uint32_t)ok) : "memory");
-    return all != 0;
-}
-
 template <typename T, int DP>
 __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnArgs g) {
     constexpr int NS = ta_slots(DP);
@@ -420,7 +396,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
     uint32_t part_no = 0;
     auto told_part = [&]() {
         return __all_sync(0xFFFFFFFFu,
-                          ta_wait(pfull_seg + part_no % kTaSegs, (part_no / kTaSegs) & 1, abort_flag));
+                          tc_wait_long(pfull_seg + part_no % kTaSegs, (part_no / kTaSegs) & 1, abort_flag));
     };
     auto drop = [&]() {
         __syncwarp();
@@ -538,7 +514,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                         if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(empty + st, par))) {
                             cp_async_wait<0>();          // nothing more to begin: hand over what is there
                             signal(u);
-                            ok = __all_sync(0xFFFFFFFFu, ta_wait(empty + st, par, abort_flag));
+                            ok = __all_sync(0xFFFFFFFFu, tc_wait_long(empty + st, par, abort_flag));
                             if (!ok) break;
                         }
                     }
@@ -598,7 +574,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
             for (uint32_t n = 0;; ++n) {
                 TaSeg e;
                 ta_next(g, w, e);
-                if (n >= kTaSegs && !__all_sync(0xFFFFFFFFu, ta_wait(pempty_seg + n % kTaSegs, (n / kTaSegs - 1) & 1,
+                if (n >= kTaSegs && !__all_sync(0xFFFFFFFFu, tc_wait_long(pempty_seg + n % kTaSegs, (n / kTaSegs - 1) & 1,
                                                                      abort_flag))) {
                     give_up();
                     break;
@@ -624,7 +600,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
             if (nt == 0) continue;
             if (lane == 0) {
                 auto wait = [&](uint64_t* bar, uint32_t par) {
-                    if (ok && !ta_wait(bar, par, abort_flag)) ok = false;
+                    if (ok && !tc_wait_long(bar, par, abort_flag)) ok = false;
                     tc_fence_after();
                 };
                 auto scores = [&](int acc, uint32_t st) {
@@ -683,7 +659,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
         if (lane == 0) {
             // The products in flight end before the tensor memory is freed.
             tc_commit(idle);
-            ta_wait(idle, 0, never);
+            tc_wait_long(idle, 0, never);
         }
         __syncwarp();
     }
@@ -702,7 +678,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
             // The eight warps go on, or end, together.
             if (!told_part()) ok = false;
             if (!ok) give_up();
-            if (!all_softmax(ok)) break;
+            if (!all_first256(ok)) break;
             const TaSeg& e = segs[part_no % kTaSegs];
             if (!e.more) break;
             const int xr = acc * 128 + row;              // of the unit's rows
@@ -741,7 +717,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                      (int64_t)(e.hk * a.group + (e.g0 + xr - tr * a.group)) * D;
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < e.nt && ok; ++i) {
-                ok = __all_sync(0xFFFFFFFFu, ta_wait(sfull + acc, ns & 1, abort_flag));
+                ok = __all_sync(0xFFFFFFFFu, tc_wait_long(sfull + acc, ns & 1, abort_flag));
                 ++ns;
                 if (!ok) break;
                 tc_fence_after();
@@ -823,7 +799,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 if (lane == 0) mbar_arrive(pfull + acc);
             }
             if (ok && e.nt > 0) {
-                ok = __all_sync(0xFFFFFFFFu, ta_wait(ofull + acc, (q_no - 1) & 1, abort_flag));
+                ok = __all_sync(0xFFFFFFFFu, tc_wait_long(ofull + acc, (q_no - 1) & 1, abort_flag));
                 tc_fence_after();
             }
             // The copying warps' marks on this piece reach here through the
@@ -869,9 +845,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 slot[kTaRows * DP + rr] = m;
                 slot[kTaRows * DP + kTaRows + rr] = rows_apart ? -1.f : l;
                 __threadfence();
-                bar_softmax();
+                bar_first256();
                 if (threadIdx.x == 0) *last_word = atom_add_acq_rel_gpu(g.cnt + e.c_lo, 1) == e.pieces - 1;
-                bar_softmax();
+                bar_first256();
             }
             tc_fence_before();           // the sums were read: the next piece's products may come
             bool apart = e.pieces == 1 && rows_apart;
@@ -929,7 +905,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                                                Elem<T>::pack(o[y].z * inv, o[y].w * inv));
                 }
             }
-            bar_softmax();               // everyone has read this piece's mark and the word above
+            bar_first256();               // everyone has read this piece's mark and the word above
             if (threadIdx.x == 0 && e.nt > 0) odd[(q_no - 1) & 15] = 0;
             if (apart) {
                 for (int x = warp; x < e.n_rows; x += 8) {

@@ -1,20 +1,19 @@
-// Linear attention with decay over prompts, 64 tokens at a time on the tensor
-// cores.  With b_i the sum of the log decays of a chunk's tokens up to i,
+// Linear attention with decay over prompts for k_dim over 128 (whose state does
+// not fit the tensor memory beside the other accumulators), 64 tokens at a time
+// on mma.sync.  With b_i the sum of the log decays of a chunk's tokens up to i,
 //   o_i = e^{b_i} S^T q_i + sum_{j <= i} e^{b_i - b_j} (q_i . k_j) v_j,
 //   S'  = e^{b_C} S + sum_j e^{b_C - b_j} k_j v_j^T,
 // so a chunk is four matrix products.  They are taken transposed, O^T = S^T Q^T
-// + V^T A^T and S'^T = V^T K', because then a warp's accumulators of S^T (its
-// 16 value columns as rows, all of k_dim as columns) are, register for
-// register, the A operand of the next chunk's first product: the state never
-// leaves the registers from a segment's first token to its last.
+// + V^T A^T and S'^T = V^T K', because then a warp's accumulators of S^T (16
+// value columns as rows, half of k_dim as columns) are, register for register,
+// the A operand of the next chunk's first product: the state never leaves the
+// registers from a segment's first token to its last.  The two warps of 16
+// value columns have their sums of O^T over their halves of k_dim and of the
+// tokens, and exchange half of them through shared memory; with half the state
+// each, 16 warps have room on an SM, which the products' latencies need (with 8
+// warps of the whole k_dim a scheduler issued in 38 of 100 cycles).
 //
-// Where sequences and heads alone leave SMs idle, sequences are cut into equal
-// segments: a first kernel takes what each segment adds to a state of zero (the
-// last product alone), a second one runs through the segments of every head and
-// leaves each its first state, the third computes all segments' outputs at once.
-//
-// A CTA has a warp for every 16 value columns and one more, which sums the next
-// chunk's decays meanwhile; the next chunk's rows are copied while this one's
+// The next chunk's rows are copied, and its decays summed, while this one's
 // products run, and each thread looks over the magnitudes of what it copied
 // itself, so a chunk has two barriers (three with conversions).
 //
@@ -32,15 +31,16 @@
 // on the same registers instead, where a zero weight touches nothing.
 #pragma once
 
-#include "linattn.cuh"
+#include "lin_seg.cuh"
 #include "mma_common.cuh"
 
 namespace q4 {
 
 constexpr int kLcTokens = 64;
 
-// A CTA's value columns (16 for each of nw warps) and its shared memory: two
-// buffers of Q (later the chunk's outputs), K and V, the split keys, the scores.
+// A CTA's value columns (16 for each of nw pairs of warps) and its shared memory:
+// two buffers of Q (later the chunk's outputs), K and V, the split keys, the
+// scores, and for the exchange 2 KB a warp (in K's place where that has room).
 __host__ __device__ constexpr int lc_cols(int nw) { return 16 * nw; }
 __host__ __device__ constexpr int lc_qbytes(int dk, int nw, bool out) {
     return !out ? 0 : kLcTokens * 2 * (dk > lc_cols(nw) ? dk : lc_cols(nw));
@@ -49,53 +49,12 @@ __host__ __device__ constexpr int lc_buf(int dk, int nw, bool out) {
     return lc_qbytes(dk, nw, out) + kLcTokens * 2 * (dk + lc_cols(nw));
 }
 constexpr int kLcDecay = 4 * kLcTokens + 4;          // floats of a chunk's decays
+__host__ __device__ constexpr int lc_xbytes(int dk, int nw, bool out) {
+    return !out || kLcTokens * 2 * dk >= 4096 * nw ? 0 : 4096 * nw;
+}
 __host__ __device__ constexpr int lc_smem(int dk, int nw, bool out) {
     return 2 * lc_buf(dk, nw, out) + 2 * kLcTokens * dk * 2 + (out ? kLcTokens * kLcTokens * 2 : 0) +
-           (2 * kLcDecay + 2 * 3 * 8) * 4;
-}
-
-// The segments of a prompt: `segs` for every sequence, their states and decays.
-struct LinSegArgs {
-    LinArgs a;
-    int segs;
-    float* ws;           // [n_seqs][v_heads][segs][k_dim][v_dim], then [n_seqs][v_heads][segs] decays
-};
-__device__ __forceinline__ float* seg_state(const LinSegArgs& g, int s, int h, int i) {
-    return g.ws + (((int64_t)s * g.a.v_heads + h) * g.segs + i) * g.a.k_dim * g.a.v_dim;
-}
-__device__ __forceinline__ float* seg_decay(const LinSegArgs& g, int s, int h, int i) {
-    return g.ws + (int64_t)g.a.n_seqs * g.a.v_heads * g.segs * g.a.k_dim * g.a.v_dim +
-           ((int64_t)s * g.a.v_heads + h) * g.segs + i;
-}
-// Tokens [t0, t1) of segment i of sequence s (whole chunks; later ones may be
-// empty), and whether it is the last with tokens (or the first of none).
-__device__ __forceinline__ void segment(const LinSegArgs& g, int s, int i, int64_t& t0, int64_t& t1, bool& last) {
-    int64_t lo = g.a.start[s], hi = g.a.start[s + 1];
-    if (lo < 0) lo = 0;
-    if (hi > g.a.rows) hi = g.a.rows;
-    if (hi < lo) hi = lo;
-    const int64_t chunks = (hi - lo + kLcTokens - 1) / kLcTokens;
-    const int64_t len = (chunks + g.segs - 1) / g.segs * kLcTokens;
-    t0 = lo + i * len < hi ? lo + i * len : hi;
-    t1 = lo + (i + 1) * len < hi ? lo + (i + 1) * len : hi;
-    last = t1 == hi && (t0 < t1 || i == 0);
-}
-
-__device__ __forceinline__ float exp2i(int e) {      // 2^e; 0 under and 2^127 over the range
-    return e < -126 ? 0.f : __int_as_float((min(e, 127) + 127) << 23);
-}
-// The power that brings a magnitude x >= 0 to [2^14, 2^15), `cap` at most; 0
-// for zero.
-__device__ __forceinline__ int to_2_14(float x, int cap) {
-    if (x == 0.f) return 0;
-    return min(cap, 14 - ((__float_as_int(x) >> 23) - 127));
-}
-
-__device__ __forceinline__ uint32_t max_abs8(uint32_t m, uint4 v) {      // of 16-bit floats, in halves
-    m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
-    m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
-    m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
-    return __vmaxu2(m, v.w & 0x7FFF7FFFu);
+           lc_xbytes(dk, nw, out) + (2 * kLcDecay + 2 * 3 * 16) * 4;
 }
 
 // Two 16-bit values times a power of two, as binary16.
@@ -108,11 +67,13 @@ __device__ __forceinline__ uint32_t to_half2(uint32_t v, float pw) {
 // Sums of a chunk's log decays by one warp, two tokens a lane: [64] b_i high
 // parts, [64] low parts, [64] e^{b_i}, [64] e^{b_C - b_i}, e^{b_C}, b_C.  Under
 // -104 a decay is zero in 32 bits; padding tokens do not decay.
-__device__ __forceinline__ void chunk_decays(const float* g, int64_t stride, int64_t t, int n, float* out) {
+__device__ __forceinline__ float2 decays_of(const float* g, int64_t stride, int64_t t, int64_t t1) {
+    const int64_t i = t + 2 * (threadIdx.x & 31);
+    return make_float2(i < t1 ? g[i * stride] : 0.f, i + 1 < t1 ? g[(i + 1) * stride] : 0.f);
+}
+__device__ __forceinline__ void chunk_decays(float2 g, float* out) {
     const int lane = threadIdx.x & 31;
-    double b0 = 0, b1 = 0;
-    if (2 * lane < n) b0 = g[(t + 2 * lane) * stride];
-    if (2 * lane + 1 < n) b1 = g[(t + 2 * lane + 1) * stride];
+    double b0 = g.x, b1 = g.y;
     if (b0 < -104.0) b0 = -104.0;
     if (b1 < -104.0) b1 = -104.0;
     b1 += b0;
@@ -139,25 +100,28 @@ __device__ __forceinline__ void chunk_decays(const float* g, int64_t stride, int
 // OUT: a segment's outputs and last state from its first one; else what it adds
 // to a state of zero, and its decay.
 template <typename T, int DK, int NW, bool OUT>
-__global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSegArgs g) {
+__global__ void __launch_bounds__(64 * NW, 1) lin_chunk_kernel(const LinSegArgs g) {
     constexpr bool kConvert = Elem<T>::kExpMask != Elem<__half>::kExpMask;   // bfloat16 inputs
     constexpr int C = kLcTokens;
-    constexpr int NT = 32 * NW;                          // threads of the products
+    constexpr int NT = 64 * NW;
+    constexpr int W = 2 * NW;                            // warps
     constexpr int DVS = lc_cols(NW);
     constexpr int KB = DK * 2, VB = DVS * 2;             // row bytes
-    constexpr int NK = DK / 8;                           // 8-column tiles of the state
+    constexpr int NK = DK / 16;                          // 8-column tiles of a warp's half of the state
     constexpr uint32_t BUF = lc_buf(DK, NW, OUT);
     constexpr int KCH = C * (DK / 8), VCH = C * (DVS / 8);   // 16-byte chunks of K (or Q) and V
     extern __shared__ __align__(128) uint8_t lc_raw[];
     const LinArgs& a = g.a;
     const uint32_t base = smem_addr(lc_raw);
     const uint32_t sHi = base + 2 * BUF, sLo = sHi + C * KB, sA = sLo + C * KB;
-    float* fl = reinterpret_cast<float*>(lc_raw + lc_smem(DK, NW, OUT) - (2 * kLcDecay + 48) * 4);
-    uint32_t* sMax = reinterpret_cast<uint32_t*>(fl + 2 * kLcDecay);   // [2][warp][3] largest |q|, |k|, |v|
+    float* fl = reinterpret_cast<float*>(lc_raw + lc_smem(DK, NW, OUT) - (2 * kLcDecay + 96) * 4);
+    uint32_t* sMax = reinterpret_cast<uint32_t*>(fl + 2 * kLcDecay);   // [2][16 warps][3] largest |q|, |k|, |v|
 
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, cc = lane & 3;
+    const int vg = warp >> 1, half = warp & 1;           // 16 value columns, half of k_dim
+    const int kcol = half * (DK / 2);
     const int h = blockIdx.x, c0 = blockIdx.y * DVS;
     const int s = blockIdx.z / g.segs, seg = blockIdx.z - s * g.segs;
     const int slot = a.slots ? a.slots[s] : s;
@@ -177,25 +141,8 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
     const float* gb = a.g + h;
     const int64_t so = ((int64_t)slot * a.v_heads + h) * a.k_dim * a.v_dim;
 
-    if (warp == NW) {
-        // ---- decays, a chunk ahead ----
-        double sum = 0;
-        chunk_decays(gb, a.g_stride, t0, (int)min((int64_t)C, t1 - t0), fl);
-        __syncthreads();
-        int par = 0;
-        for (int64_t t = t0; t < t1; t += C, par ^= 1) {
-            __syncwarp();
-            sum += fl[par * kLcDecay + 4 * C + 1];
-            if (t + C < t1)
-                chunk_decays(gb, a.g_stride, t + C, (int)min((int64_t)C, t1 - t - C), fl + (par ^ 1) * kLcDecay);
-            __syncthreads();
-        }
-        if (!OUT && lane == 0 && blockIdx.y == 0) *seg_decay(g, s, h, seg) = expf((float)sum);
-        return;
-    }
-
-    // The state: row warp * 16 + gr (+ 8) of its transpose, columns 8 nk + 2 cc
-    // (+ 1); S holds it times 2^E.
+    // The state: row vg * 16 + gr (+ 8) of its transpose, columns kcol + 8 nk +
+    // 2 cc (+ 1); S holds it times 2^E.
     float S[NK][4];
     int E = 0;
     const float* from = !OUT ? nullptr : g.segs > 1 ? seg_state(g, s, h, seg) : a.state_in ? a.state_in + so : nullptr;
@@ -203,7 +150,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
     for (int nk = 0; nk < NK; ++nk)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const int dv = c0 + warp * 16 + gr + 8 * (x >> 1), dk = 8 * nk + 2 * cc + (x & 1);
+            const int dv = c0 + vg * 16 + gr + 8 * (x >> 1), dk = kcol + 8 * nk + 2 * cc + (x & 1);
             S[nk][x] = from && dv < a.v_dim && dk < a.k_dim ? from[(int64_t)dk * a.v_dim + dv] : 0.f;
         }
 
@@ -250,10 +197,14 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
             if (lane == 0) mx[3 * warp + y] = m[y];
         }
     };
-    auto bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
+    // The pair of warps with the same value columns.
+    auto bar_pair = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + vg) : "memory"); };
+    const bool sums = warp == W - 1;                     // this warp sums the decays
+    double total = 0;
 
     if (t0 < t1) {
         copy(t0, base);
+        if (sums) chunk_decays(decays_of(gb, a.g_stride, t0, t1), fl);
         arrived(base, sMax);
     }
     __syncthreads();
@@ -264,13 +215,21 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
         const float* dec = fl + par * kLcDecay;
         const float *sBh = dec, *sBl = dec + C, *sEb = dec + 2 * C, *sW = dec + 3 * C;
         if (t + C < t1) copy(t + C, base + (par ^ 1) * BUF);
+        float2 g_next = make_float2(0.f, 0.f);
+        if (sums) {
+            g_next = decays_of(gb, a.g_stride, t + C, t1);
+            total += dec[4 * C + 1];
+        }
+        auto next_decays = [&]() {
+            if (sums && t + C < t1) chunk_decays(g_next, fl + (par ^ 1) * kLcDecay);
+        };
 
         float big[3];
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
-            uint32_t m = sMax[24 * par + x];
+            uint32_t m = sMax[48 * par + x];
 #pragma unroll
-            for (int y = 1; y < NW; ++y) m = __vmaxu2(m, sMax[24 * par + 3 * y + x]);
+            for (int y = 1; y < W; ++y) m = __vmaxu2(m, sMax[48 * par + 3 * y + x]);
             const float2 f = Elem<T>::unpack(m);
             big[x] = fmaxf(f.x, f.y);
             if (!(f.x < 1073741824.f && f.y < 1073741824.f)) big[x] = INFINITY;        // NaN too
@@ -284,12 +243,15 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
             for (int nk = 0; nk < NK; ++nk)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) S[nk][x] *= un;
+            next_decays();
+            // The halves' sums of an output meet through the scores' place.
+            float* px = reinterpret_cast<float*>(lc_raw + (sA - base)) + vg * 32;
             for (int r = 0; r < n; ++r) {
                 const float d = expf(gb[(t + r) * a.g_stride]);
                 float v[2], o[2] = {0.f, 0.f};
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int c = warp * 16 + gr + 8 * y;
+                    const int c = vg * 16 + gr + 8 * y;
                     uint32_t u;
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u)
                                  : "r"(sV + (uint32_t)(r * VB + (((c >> 3) ^ (r & 7)) << 4) + ((c & 6) << 1))));
@@ -298,7 +260,8 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
                 }
 #pragma unroll
                 for (int nk = 0; nk < NK; ++nk) {
-                    const uint32_t at = (uint32_t)(r * KB + ((nk ^ (r & 7)) << 4) + 4 * cc);
+                    const int kc = kcol / 8 + nk;
+                    const uint32_t at = (uint32_t)(r * KB + ((kc ^ (r & 7)) << 4) + 4 * cc);
                     uint32_t uq = 0, uk;
                     if (OUT) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(uq) : "r"(sQ + at));
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(uk) : "r"(sK + at));
@@ -309,21 +272,27 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
                         float& s1 = S[nk][2 * y + 1];
                         s0 = fmaf(s0, d, k.x * v[y]);
                         s1 = fmaf(s1, d, k.y * v[y]);
-                        if (OUT && 8 * nk + 2 * cc < a.k_dim) {
+                        if (OUT && 8 * kc + 2 * cc < a.k_dim) {
                             o[y] = fmaf(q.x * a.scale, s0, o[y]);
                             o[y] = fmaf(q.y * a.scale, s1, o[y]);
                         }
                     }
                 }
-                if (OUT)
+                if constexpr (OUT) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float f = o[y];
-                        f += __shfl_xor_sync(0xFFFFFFFFu, f, 1);
-                        f += __shfl_xor_sync(0xFFFFFFFFu, f, 2);
-                        const int c = warp * 16 + gr + 8 * y;
-                        if (cc == 0 && c0 + c < a.v_dim) ob[(t + r) * a.o_stride + c] = Elem<T>::round(f);
+                        o[y] += __shfl_xor_sync(0xFFFFFFFFu, o[y], 1);
+                        o[y] += __shfl_xor_sync(0xFFFFFFFFu, o[y], 2);
+                        if (half && cc == 0) px[16 * (r & 1) + gr + 8 * y] = o[y];
                     }
+                    bar_pair();
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int c = vg * 16 + gr + 8 * y;
+                        if (!half && cc == 0 && c0 + c < a.v_dim)
+                            ob[(t + r) * a.o_stride + c] = Elem<T>::round(o[y] + px[16 * (r & 1) + gr + 8 * y]);
+                    }
+                }
             }
         } else {
             // Powers: q, v (and k of the scores) times 2^sq, 2^sv (2^skk) in
@@ -369,14 +338,14 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
                 sts128(sLo + 16u * x, make_uint4(lo[0], lo[1], lo[2], lo[3]));
                 if (kConvert && OUT) sts128(sK + 16u * x, make_uint4(kk[0], kk[1], kk[2], kk[3]));
             }
-            if (kConvert) bar();
+            if (kConvert) __syncthreads();
 
             float O[OUT ? C / 8 : 1][4];
             if constexpr (OUT) {
                 // Scores of the ten 16 x 16 blocks on and under the diagonal in
                 // halves of eight columns, each with its decays, as the
                 // transposed product's B operand [i][j].
-                for (int hb = warp; hb < 20; hb += NW) {
+                for (int hb = warp; hb < 20; hb += W) {
                     const int blk = hb >> 1;
                     const int bi = blk == 0 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bj = blk - bi * (bi + 1) / 2;
                     if (16 * bi >= n) continue;
@@ -409,8 +378,8 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
                     }
                 }
 
-                // O^T = (S^T 2^row) Q^T, then brought to the scores' scale with
-                // the decays e^{b_i}.
+                // O^T = (S^T 2^row) Q^T over this half of k_dim, then brought to
+                // the scores' scale with the decays e^{b_i}.
 #pragma unroll
                 for (int x = 0; x < C / 8; ++x)
 #pragma unroll
@@ -429,7 +398,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
                     rp[y] = exp2i(rs[y]);
                 }
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) {
+                for (int kk = 0; kk < DK / 32; ++kk) {
                     uint32_t af[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
@@ -440,7 +409,7 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
 #pragma unroll
                     for (int np = 0; np < C / 16; ++np) {
                         uint32_t bf[4];
-                        const int rb = 16 * np + (lane & 7) + ((lane >> 4) << 3), cb = 2 * kk + ((lane >> 3) & 1);
+                        const int rb = 16 * np + (lane & 7) + ((lane >> 4) << 3), cb = kcol / 8 + 2 * kk + ((lane >> 3) & 1);
                         ldmatrix4(bf, sQ + (uint32_t)(rb * KB + ((cb ^ (rb & 7)) << 4)));
                         mma16816<__half>(O[2 * np], af, bf[0], bf[1]);
                         mma16816<__half>(O[2 * np + 1], af, bf[2], bf[3]);
@@ -467,7 +436,8 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
                     for (int x = 0; x < 4; ++x) S[nk][x] = S[nk][x] * decay * f1;
                 E = sk + sv;
             }
-            bar();
+            next_decays();
+            __syncthreads();
 
             // O^T += V^T A^T and S^T += V^T K' (both parts), 16 tokens at a time.
 #pragma unroll
@@ -477,10 +447,12 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
                     {
                         // transposed blocks: value columns 0-7, 8-15 at tokens 0-7, then at 8-15
                         const int r = 16 * kt + (lane & 7) + ((lane >> 4) << 3);
-                        const int ch = 2 * warp + ((lane >> 3) & 1);
+                        const int ch = 2 * vg + ((lane >> 3) & 1);
                         ldmatrix4t(vf, sV + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4)));
                     }
-                    if constexpr (OUT) {
+                    // Of the scores' product each warp of the pair takes half:
+                    // tokens 0-15 and 48-63, or 16-47.
+                    if (OUT && (kt == 0 || kt == 3) == (half == 0)) {
 #pragma unroll
                         for (int np = kt; np < C / 16; ++np) {
                             const int rb = 16 * np + (lane & 7) + ((lane >> 4) << 3), cb = 2 * kt + ((lane >> 3) & 1);
@@ -493,9 +465,9 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
                         }
                     }
 #pragma unroll
-                    for (int np = 0; np < DK / 16; ++np) {
+                    for (int np = 0; np < DK / 32; ++np) {
                         uint32_t hf[4], lf[4];
-                        const int r = 16 * kt + (lane & 15), ch = 2 * np + (lane >> 4);
+                        const int r = 16 * kt + (lane & 15), ch = kcol / 8 + 2 * np + (lane >> 4);
                         const uint32_t at = (uint32_t)(r * KB + ((ch ^ (r & 7)) << 4));
                         ldmatrix4t(hf, sHi + at);
                         ldmatrix4t(lf, sLo + at);
@@ -508,35 +480,60 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
             }
 
             if constexpr (OUT) {
-                // Outputs: transposed into the queries' place, then out in rows.
+                // The pair's sums: each warp gives the other its sums of 32 of the
+                // tokens and finishes the 32 others (0-31 the first warp).
+                float* xb = reinterpret_cast<float*>(lc_raw + ((lc_xbytes(DK, NW, OUT) ? sA + C * C * 2 : sK) - base));
+                {
+                    float4* px = reinterpret_cast<float4*>(xb + warp * 512) + lane;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        px[32 * x] = make_float4(half ? O[x][0] : O[4 + x][0], half ? O[x][1] : O[4 + x][1],
+                                                 half ? O[x][2] : O[4 + x][2], half ? O[x][3] : O[4 + x][3]);
+                    }
+                }
+                bar_pair();
+                float M[4][4];
+                {
+                    const float4* px = reinterpret_cast<const float4*>(xb + (warp ^ 1) * 512) + lane;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float4 v = px[32 * x];
+                        M[x][0] = (half ? O[4 + x][0] : O[x][0]) + v.x;
+                        M[x][1] = (half ? O[4 + x][1] : O[x][1]) + v.y;
+                        M[x][2] = (half ? O[4 + x][2] : O[x][2]) + v.z;
+                        M[x][3] = (half ? O[4 + x][3] : O[x][3]) + v.w;
+                    }
+                }
+                // Transposed into the queries' place, then out in rows.
                 const float fo = exp2i(ta - sq - skk - sv) * a.scale;
 #pragma unroll
-                for (int np = 0; np < C / 16; ++np) {
+                for (int np = 0; np < 2; ++np) {
                     // blocks: (columns 0-7, tokens 0-7), (columns 8-15, tokens 0-7), the same of tokens 8-15
                     uint32_t p[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const float* o = O[2 * np + (x >> 1)];
+                        const float* o = M[2 * np + (x >> 1)];
                         p[x] = Elem<T>::pack(o[2 * (x & 1)] * fo, o[2 * (x & 1) + 1] * fo);
                     }
-                    const int r = 16 * np + (lane & 7) + ((lane >> 4) << 3);
-                    const int ch = 2 * warp + ((lane >> 3) & 1);
+                    const int r = 32 * half + 16 * np + (lane & 7) + ((lane >> 4) << 3);
+                    const int ch = 2 * vg + ((lane >> 3) & 1);
                     stmatrix4t(sQ + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4)), p[0], p[1], p[2], p[3]);
                 }
                 __syncwarp();
 #pragma unroll
-                for (int x = 0; x < C * 2 / 32; ++x) {
-                    const int r = (x * 32 + lane) / 2, ch = 2 * warp + (lane & 1);
+                for (int x = 0; x < 2; ++x) {
+                    const int r = 32 * half + 16 * x + (lane >> 1), ch = 2 * vg + (lane & 1);
                     const uint4 v = lds128(sQ + (uint32_t)(r * VB + ((ch ^ (r & 7)) << 4)));
                     if (r < n && c0 + 8 * ch < a.v_dim)
                         *reinterpret_cast<uint4*>(ob + (t + r) * a.o_stride + 8 * ch) = v;
                 }
             }
         }
-        if (t + C < t1) arrived(base + (par ^ 1) * BUF, sMax + 24 * (par ^ 1));
+        if (t + C < t1) arrived(base + (par ^ 1) * BUF, sMax + 48 * (par ^ 1));
         __syncthreads();
     }
 
+    if (!OUT && sums && lane == 0 && blockIdx.y == 0) *seg_decay(g, s, h, seg) = expf((float)total);
     float* to = OUT ? (last ? a.state_out + so : nullptr) : seg_state(g, s, h, seg);
     if (!to) return;
     const float un = exp2i(-E);
@@ -544,57 +541,9 @@ __global__ void __launch_bounds__(32 * (NW + 1), 1) lin_chunk_kernel(const LinSe
     for (int nk = 0; nk < NK; ++nk)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const int dv = c0 + warp * 16 + gr + 8 * (x >> 1), dk = 8 * nk + 2 * cc + (x & 1);
+            const int dv = c0 + vg * 16 + gr + 8 * (x >> 1), dk = kcol + 8 * nk + 2 * cc + (x & 1);
             if (dv < a.v_dim && dk < a.k_dim) to[(int64_t)dk * a.v_dim + dv] = S[nk][x] * un;
         }
-}
-
-// The segments' first states: in each place of a segment's gain, the state
-// that it starts from.
-constexpr int kLinScanThreads = 128;
-static __global__ void __launch_bounds__(kLinScanThreads) lin_scan_kernel(const LinSegArgs g) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const LinArgs& a = g.a;
-    const int h = blockIdx.y, s = blockIdx.z;
-    const int slot = a.slots ? a.slots[s] : s;
-    if ((unsigned)slot >= (unsigned)a.n_slots) return;           // reported by the segments' kernel
-    const int64_t e = ((int64_t)blockIdx.x * kLinScanThreads + threadIdx.x) * 4, size = (int64_t)a.k_dim * a.v_dim;
-    if (e >= size) return;
-    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.state_in) S = *reinterpret_cast<const float4*>(a.state_in + ((int64_t)slot * a.v_heads + h) * size + e);
-    int n = g.segs;                                              // segments that have a gain
-    for (int i = 0; i < g.segs; ++i) {
-        int64_t t0, t1;
-        bool last;
-        segment(g, s, i, t0, t1, last);
-        if (last) {
-            n = i;
-            break;
-        }
-    }
-    float* p = seg_state(g, s, h, 0) + e;
-    constexpr int kAhead = 4;
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
-        float4 d[kAhead];
-        float w[kAhead];
-#pragma unroll
-        for (int y = 0; y < kAhead; ++y)
-            if (i0 + y < n) {
-                d[y] = *reinterpret_cast<const float4*>(p + (i0 + y) * size);
-                w[y] = *seg_decay(g, s, h, i0 + y);
-            }
-#pragma unroll
-        for (int y = 0; y < kAhead; ++y)
-            if (i0 + y < n) {
-                *reinterpret_cast<float4*>(p + (i0 + y) * size) = S;
-                S.x = fmaf(S.x, w[y], d[y].x);
-                S.y = fmaf(S.y, w[y], d[y].y);
-                S.z = fmaf(S.z, w[y], d[y].z);
-                S.w = fmaf(S.w, w[y], d[y].w);
-            }
-    }
-    if (n < g.segs) *reinterpret_cast<float4*>(p + n * size) = S;
 }
 
 }  // namespace q4

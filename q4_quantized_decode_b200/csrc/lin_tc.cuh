@@ -1,0 +1,598 @@
+// Linear attention with decay over prompts on the 5th-generation tensor cores,
+// 128 tokens at a time.  With b_i the sum of the log decays of a chunk's tokens
+// up to i,
+//   o_i = e^{b_i} q_i S + sum_{j <= i} e^{b_i - b_j} (q_i . k_j) v_j,
+//   S'  = e^{b_C} S + sum_j e^{b_C - b_j} k_j v_j^T,
+// a chunk is four products with all accumulators in tensor memory: the scores
+// Q K^T, the part of the outputs from the state, the part from the chunk, and
+// what the state gains (the state stays there, as S^T: a value column a lane).
+//   warps 0-7  the passes between the products, a thread half a row: the state
+//              to a 16-bit operand in shared memory and times its decay in
+//              place; the scores times their decays, to the 16-bit operand in
+//              their own place; the decayed keys k' = e^{b_C - b_j} k_j split
+//              into 16-bit parts; values looked over; outputs out
+//   warp 8     one thread issues the products
+//   warp 9     one thread loads Q, K and V by tensor map, K a chunk ahead
+//   warp 10    sums of the log decays, a chunk ahead
+// What bounds it: the passes, about 5 instructions for each of 5 x 16384 values
+// of a chunk, twice the 2560 cycles of the products.
+//
+// Number formats.  State and sums are in 32 bits.  The split keys carry 22
+// (binary16: two parts) or 24 (bfloat16: three) significant bits into the
+// state; one part alone would leave it with 11 or 8.  The state's and the
+// scores' operands of the output products are rounded once to the type, as the
+// output itself is.  In binary16 powers of two keep them inside its range: of
+// the chunk's largest key, of the state's largest value in a column, of a row's
+// largest score.  Sums of log decays are in 64 bits (differences of far-apart
+// sums).  A value that is not finite must not meet the zero weight of an
+// earlier token: it is replaced by zero for the products, and the outputs and
+// state columns that it does reach are set to NaN.
+//
+// Long sequences run as parallel segments (lin_seg.cuh).
+#pragma once
+
+#include <cuda.h>
+
+#include "lin_seg.cuh"
+#include "mma_common.cuh"
+#include "tc_common.cuh"
+
+namespace q4 {
+
+constexpr int kLtTokens = 128;
+constexpr int kLtThreads = 32 * 12;
+constexpr uint32_t kLtHalf = kLtTokens * 128;        // [128 rows][64 elements]
+constexpr int kLtDec = 4 * kLtTokens + 4;            // floats of a chunk's decays
+
+__host__ __device__ constexpr int lt_kbytes(int dk) { return kLtTokens * dk * 2; }
+// Q, two K's, V, the keys' second part, the state's operand.
+__host__ __device__ constexpr int lt_smem(int dk, bool out) {
+    return 1024 + (out ? 2 : 0) * lt_kbytes(dk) + 3 * lt_kbytes(dk) + 2 * (int)kLtHalf + (out ? 0 : lt_kbytes(dk)) +
+           2 * kLtDec * 4 + (4 * 128 + 128 + 2 * 128 + 16) * 4 + 256;
+}
+
+struct LinTcArgs {
+    LinSegArgs g;
+    uint32_t idesc_a, idesc_i, idesc_o, idesc_s;     // of the four products
+    CUtensorMap qmap, kmap, vmap;                    // [row][head][element], boxes of 64 elements x 128 rows
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// Sums of a chunk's log decays by one warp, four tokens a lane, in units of
+// log2: [128] b_i high parts, [128] low parts, [128] e^{b_i}, [128] e^{b_C -
+// b_i}, e^{b_C}, b_C.  Under -104 a decay is zero in 32 bits; padding tokens do
+// not decay.
+__device__ __forceinline__ void lt_decays(float4 g, float* out) {
+    const int lane = threadIdx.x & 31;
+    double b[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (b[i] < -104.0) b[i] = -104.0;
+        if (i) b[i] += b[i - 1];
+    }
+    double p = b[3];
+    for (int d = 1; d < 32; d <<= 1) {
+        const double y = __shfl_up_sync(0xFFFFFFFFu, p, d);
+        if (lane >= d) p += y;
+    }
+    const double before = p - b[3], all = __shfl_sync(0xFFFFFFFFu, p, 31);
+    float hi[4], lo[4], e[4], w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const double x = b[i] + before, x2 = x * 1.4426950408889634074;
+        hi[i] = (float)x2;
+        lo[i] = (float)(x2 - hi[i]);
+        e[i] = expf((float)x);
+        w[i] = expf((float)(all - x));
+    }
+    float4* o = reinterpret_cast<float4*>(out) + lane;
+    o[0] = make_float4(hi[0], hi[1], hi[2], hi[3]);
+    o[32] = make_float4(lo[0], lo[1], lo[2], lo[3]);
+    o[64] = make_float4(e[0], e[1], e[2], e[3]);
+    o[96] = make_float4(w[0], w[1], w[2], w[3]);
+    if (lane == 0) {
+        out[4 * kLtTokens] = expf((float)all);
+        out[4 * kLtTokens + 1] = (float)all;
+    }
+}
+
+template <typename T, int DK, bool OUT>
+__global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_constant__ LinTcArgs ta) {
+    constexpr bool kHalf16 = Elem<T>::kExpMask == Elem<__half>::kExpMask;
+    constexpr int C = kLtTokens;
+    constexpr uint32_t KB = lt_kbytes(DK);
+    constexpr int CW = DK / 2;                           // state columns of a thread
+    constexpr uint32_t kColA = 128, kColI = 256, kColO = 384;   // TMEM: state at 0, scores, outputs' two parts
+    extern __shared__ uint8_t lt_raw[];
+    const LinSegArgs& g = ta.g;
+    const LinArgs& a = g.a;
+    const uint32_t raw0 = smem_addr(lt_raw);
+    const uint32_t sK = (raw0 + 1023u) & ~1023u;         // two
+    const uint32_t sX = sK + 2 * KB;                     // the keys' second part
+    const uint32_t sV = sX + KB;
+    const uint32_t sQ = sV + 2 * kLtHalf;                // with OUT; the third part (bfloat16) in its place, or after V
+    const uint32_t sS = sQ + KB;                         // the state's operand, with OUT
+    float* fl = reinterpret_cast<float*>(lt_raw + ((OUT ? sS + KB : sQ + KB) - raw0));
+    float* sx = fl + 2 * kLtDec;                         // [2][128] row maxima of the halves: state, scores
+    float* sy = sx + 256;
+    float* colf = sy + 256;                              // [128] scale of a value column of the state's operand
+    volatile int* badc = reinterpret_cast<volatile int*>(colf + 128);   // [2][128] first token with a bad value, or 128
+    uint32_t* sMax = reinterpret_cast<uint32_t*>(colf + 384);           // [8] largest |k|
+    volatile int* any_bad = reinterpret_cast<volatile int*>(sMax + 8);  // [2]
+    volatile int* abort_flag = any_bad + 2;
+    volatile int* never = any_bad + 3;
+    uint32_t* tslot = sMax + 12;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sMax + 16);
+    uint64_t *kfull = bars, *qfull = bars + 2, *vfull = bars + 3, *dfull = bars + 4, *dfree = bars + 6, *qkdone = bars + 8,
+             *qfree = bars + 9, *odone = bars + 10, *kvdone = bars + 11, *sready = bars + 12, *pready = bars + 13,
+             *kready = bars + 14, *oread = bars + 15, *idle = bars + 16;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(kfull + i, 1);
+            mbar_init(dfull + i, 1);
+            mbar_init(dfree + i, 8);
+            any_bad[i] = 0;
+        }
+        for (uint64_t* b : {qfull, vfull, qkdone, qfree, odone, kvdone, idle}) mbar_init(b, 1);
+        for (uint64_t* b : {sready, pready, kready, oread}) mbar_init(b, 8);
+        *abort_flag = *never = 0;
+        fence_barrier_init();
+    }
+    if (threadIdx.x < 256) badc[threadIdx.x] = C;
+    if (warp == 8) tc_alloc(tslot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const int h = blockIdx.x, c0 = blockIdx.y * 128;
+    const int s = blockIdx.z / g.segs, seg = blockIdx.z - s * g.segs;
+    const int slot = a.slots ? a.slots[s] : s;
+    const bool bad_slot = (unsigned)slot >= (unsigned)a.n_slots;
+    if (bad_slot && threadIdx.x == 0) set_device_error(a.err, kDevIndex);
+    int64_t t0 = 0, t1 = 0;
+    bool last = false;
+    if (!bad_slot) segment(g, s, seg, t0, t1, last);
+    const bool work = !bad_slot && (OUT ? t0 < t1 || last : t0 < t1 && !last);
+    const int nc = work ? (int)((t1 - t0 + C - 1) / C) : 0;
+    const int hk = h / a.each;
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        set_device_error(a.err, kDevTimeout);
+    };
+
+    if (warp == 9) {
+        // ---- loads ----
+        if (lane == 0) {
+            bool ok = true;
+            int nk = 0, nq = 0, nv = 0;                  // loads begun
+            for (int c = 0; c < nc && ok; ++c) {
+                const int t = (int)(t0 + (int64_t)c * C);
+                // K's buffer was chunk c - 2's, whose last product was waited for below.
+                mbar_arrive_expect_tx(kfull + (c & 1), KB);
+                for (int i = 0; i < DK / 64; ++i)
+                    tma_load_3d(sK + (c & 1) * KB + i * kLtHalf, &ta.kmap, 64 * i, hk, t, kfull + (c & 1));
+                ++nk;
+                if (OUT && kHalf16) {
+                    if (c > 0) ok = tc_wait_long(qfree, (c - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(qfull, KB);
+                    for (int i = 0; i < DK / 64; ++i) tma_load_3d(sQ + i * kLtHalf, &ta.qmap, 64 * i, hk, t, qfull);
+                    ++nq;
+                }
+                if (c > 0) ok = tc_wait_long(kvdone, (c - 1) & 1, abort_flag);
+                if (!ok) break;
+                if (OUT && !kHalf16) {
+                    mbar_arrive_expect_tx(qfull, KB);
+                    for (int i = 0; i < DK / 64; ++i) tma_load_3d(sQ + i * kLtHalf, &ta.qmap, 64 * i, hk, t, qfull);
+                    ++nq;
+                }
+                mbar_arrive_expect_tx(vfull, 2 * kLtHalf);
+                for (int i = 0; i < 2; ++i) tma_load_3d(sV + i * kLtHalf, &ta.vmap, c0 + 64 * i, h, t, vfull);
+                ++nv;
+            }
+            if (!ok) give_up();
+            // Copies in flight land before the CTA ends (in vain only after a
+            // wait that gave up).
+            for (int i = 0; i < 2; ++i)
+                if (nk > i) tc_wait_long(kfull + i, ((nk + 1 - i) / 2 - 1) & 1, never);
+            if (nq > 0) tc_wait_long(qfull, (nq - 1) & 1, never);
+            if (nv > 0) tc_wait_long(vfull, (nv - 1) & 1, never);
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ---- decays ----
+        double total = 0;
+        bool ok = true;
+        const float* gb = a.g + h;
+        auto load = [&](int c) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t t = t0 + (int64_t)c * C + 4 * lane + i;
+                v[i] = c < nc && t < t1 ? gb[t * a.g_stride] : 0.f;
+            }
+            return make_float4(v[0], v[1], v[2], v[3]);
+        };
+        float4 next = load(0);
+        for (int c = 0; c < nc; ++c) {
+            const float4 now = next;
+            next = load(c + 1);
+            if (c >= 2) ok = __all_sync(0xFFFFFFFFu, tc_wait_long(dfree + (c & 1), ((c >> 1) - 1) & 1, abort_flag));
+            if (!ok) break;
+            float* d = fl + (c & 1) * kLtDec;
+            lt_decays(now, d);
+            __syncwarp();
+            total += d[4 * C + 1];
+            if (lane == 0) mbar_arrive(dfull + (c & 1));
+        }
+        if (!ok) give_up();
+        if (!OUT && work && lane == 0 && blockIdx.y == 0) *seg_decay(g, s, h, seg) = expf((float)total);
+    } else if (warp == 8) {
+        // ---- products ----
+        if (lane == 0) {
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t par) {
+                if (ok && !tc_wait_long(bar, par & 1, abort_flag)) ok = false;
+                tc_fence_after();
+                return ok;
+            };
+            for (int c = 0; c < nc && ok; ++c) {
+                const uint32_t k = sK + (c & 1) * KB;
+                if (OUT) {
+                    wait(kfull + (c & 1), c >> 1);
+                    if (!wait(qfull, c)) break;
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk) {
+                        const uint32_t o = (uint32_t)(kk >> 2) * kLtHalf + 32u * (kk & 3);
+                        tc_mma_f16(tmem + kColA, tc_sdesc_sw128(sQ + o), tc_sdesc_sw128(k + o), ta.idesc_a, kk != 0);
+                    }
+                    tc_commit(qkdone);
+                    wait(sready, c);
+                    if (c > 0) wait(oread, c - 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk) {
+                        const uint32_t o = (uint32_t)(kk >> 2) * kLtHalf + 32u * (kk & 3);
+                        tc_mma_f16(tmem + kColI, tc_sdesc_sw128(sQ + o), tc_sdesc_sw128(sS + o), ta.idesc_i, kk != 0);
+                    }
+                    tc_commit(qfree);
+                    wait(vfull, c);
+                    if (!wait(pready, c)) break;
+#pragma unroll
+                    for (int kk = 0; kk < C / 16; ++kk)
+                        tc_mma_f16_ta(tmem + kColO, tmem + kColA + 8u * kk, tc_sdesc_sw128_nmajor(sV + 2048u * kk, kLtHalf),
+                                      ta.idesc_o, kk != 0);
+                    tc_commit(odone);
+                }
+                wait(vfull, c);
+                if (!wait(kready, c)) break;
+                const uint32_t parts[3] = {k, sX, sQ};
+#pragma unroll
+                for (int p = 0; p < (kHalf16 ? 2 : 3); ++p)
+#pragma unroll
+                    for (int kk = 0; kk < C / 16; ++kk)
+                        tc_mma_f16(tmem, tc_sdesc_sw128_nmajor(sV + 2048u * kk, kLtHalf),
+                                   tc_sdesc_sw128_nmajor(parts[p] + 2048u * kk, kLtHalf), ta.idesc_s, 1u);
+                tc_commit(kvdone);
+            }
+            if (!ok) give_up();
+            tc_commit(idle);
+            tc_wait_long(idle, 0, never);
+        }
+        __syncwarp();
+    } else if (warp < 8 && work) {
+        // ---- passes: lane quadrant warp % 4, column half warp / 4 ----
+        const int row = 32 * (warp & 3) + lane, hc = warp >> 2, tid = threadIdx.x;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + (uint32_t)(hc * CW);
+        const bool real = c0 + row < a.v_dim;            // this thread's value column, in the state's passes
+        const int64_t so = ((int64_t)slot * a.v_heads + h) * a.k_dim * a.v_dim;
+        const float* from = !OUT ? nullptr : g.segs > 1 ? seg_state(g, s, h, seg) : a.state_in ? a.state_in + so : nullptr;
+        float* to = OUT ? (last ? a.state_out + so : nullptr) : seg_state(g, s, h, seg);
+        if (from) from += c0 + row;
+        if (to) to += c0 + row;
+        // The first state.
+#pragma unroll 1
+        for (int x = 0; x < CW; x += 32) {
+            uint32_t v[32];
+#pragma unroll
+            for (int y = 0; y < 32; ++y) {
+                const int dk = hc * CW + x + y;
+                v[y] = from && real && dk < a.k_dim ? __float_as_uint(from[(int64_t)dk * a.v_dim]) : 0u;
+                if (nc == 0 && to && real && dk < a.k_dim) to[(int64_t)dk * a.v_dim] = __uint_as_float(v[y]);
+            }
+            tc_st32(tS + x, v);
+        }
+        tc_wait_st();
+        int E = 0;                                       // TMEM holds the state times 2^E
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t par) {
+            if (ok && !tc_wait_long(bar, par & 1, abort_flag)) ok = false;
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) give_up();
+        };
+        auto tell = [&](uint64_t* bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        T* ob = static_cast<T*>(a.out) + (int64_t)h * a.v_dim + c0 + 64 * hc;
+        for (int c = 0; c < nc; ++c) {
+            const int64_t t = t0 + (int64_t)c * C;
+            const int n = (int)min((int64_t)C, t1 - t);
+            const uint32_t k = sK + (c & 1) * KB;
+            const float* dec = fl + (c & 1) * kLtDec;
+            const int bad_now = 128 * (c & 1), bad_then = 128 * ((c & 1) ^ 1);
+
+            // The chunk's largest key, and the common end after a wait that gave up.
+            wait(kfull + (c & 1), c >> 1);
+            if (kHalf16) {
+                uint32_t m = 0;
+#pragma unroll 4
+                for (int x = tid; x < (int)KB / 16; x += 256)
+                    if (((x >> 3) & 127) < n) m = max_abs8(m, lds128(k + 16u * x));
+                for (int x = 16; x; x >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+                if (lane == 0) sMax[warp] = m;
+            }
+            wait(dfull + (c & 1), c >> 1);
+            if (!all_first256(ok)) break;
+            int sk = 0;
+            if (kHalf16) {
+                uint32_t m = sMax[0];
+#pragma unroll
+                for (int y = 1; y < 8; ++y) m = __vmaxu2(m, sMax[y]);
+                const uint32_t top = max(m & 0xFFFFu, m >> 16);
+                // The largest to [2^14, 2^15); with infinities or NaN, what suits any finite key.
+                sk = top >= Elem<__half>::kExpMask ? -2
+                                                   : to_2_14(__half2float(__ushort_as_half((unsigned short)top)), 24);
+            }
+
+            // The state: its operand, and its decay.
+            if (c > 0) wait(kvdone, c - 1);
+            tc_fence_after();
+            const bool spoilt = any_bad[(c & 1) ^ 1] && badc[bad_then + row] < C;   // by the last chunk's values
+            const float decay = dec[4 * C], f1 = exp2i(sk - E);
+            float rp = 1.f;
+            float sv[CW / 32][32];
+#pragma unroll
+            for (int x = 0; x < CW / 32; ++x) tc_ld32(tS + 32u * x, sv[x]);
+#pragma unroll
+            for (int x = 0; x < CW / 32; ++x) tc_wait_ld(sv[x]);
+            if (spoilt)
+#pragma unroll
+                for (int x = 0; x < CW / 32; ++x)
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) sv[x][y] = __int_as_float(0x7FFFFFFF);
+            if (OUT && kHalf16) {
+                float m = 0.f;
+#pragma unroll
+                for (int x = 0; x < CW / 32; ++x)
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) m = fmaxf(m, fabsf(sv[x][y]));
+                sx[128 * hc + row] = m;
+                bar_first256();
+                m = fmaxf(m, sx[128 * (hc ^ 1) + row]);
+                const int e = (__float_as_int(m) >> 23) - 127;
+                const int rs = m == 0.f || e > 127 ? 0 : min(126, 14 - e);
+                rp = exp2i(rs);
+                if (hc == 0) colf[row] = exp2i(-rs - E);
+            } else if (OUT) {
+                if (hc == 0) colf[row] = 1.f;
+                bar_first256();
+            } else {
+                bar_first256();
+            }
+            if (hc == 0 && spoilt) badc[bad_then + row] = C;
+            if (tid == 0) any_bad[(c & 1) ^ 1] = 0;
+            if (OUT) {
+#pragma unroll
+                for (int x = 0; x < CW / 8; ++x) {
+                    float v[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) v[y] = sv[x / 4][8 * (x % 4) + y] * rp;
+                    const int ch = hc * (CW / 8) + x;    // 16-byte chunk of the row
+                    sts128(sS + (uint32_t)(ch >> 3) * kLtHalf + (uint32_t)(row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
+                           pack8<T>(v));
+                }
+                fence_proxy_async_smem();
+            }
+#pragma unroll
+            for (int x = 0; x < CW / 32; ++x) {
+                uint32_t v[32];
+#pragma unroll
+                for (int y = 0; y < 32; ++y) v[y] = __float_as_uint(sv[x][y] * decay * f1);
+                tc_st32(tS + 32u * x, v);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            E = sk;
+            tell(sready);
+
+            // Values: rows behind the chunk's tokens to zero, and those that
+            // are not finite, which are remembered.
+            wait(vfull, c);
+            {
+                bool changed = false;
+#pragma unroll 4
+                for (int x = tid; x < (int)(2 * kLtHalf / 16); x += 256) {
+                    const int r = (x >> 3) & 127;
+                    if (r >= n) {
+                        sts128(sV + 16u * x, make_uint4(0, 0, 0, 0));
+                        changed = true;
+                    } else {
+                        const uint4 v = lds128(sV + 16u * x);
+                        if (any_nonfinite<T>(v)) {
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            const int col = 64 * (x >> 10) + 8 * ((x & 7) ^ (r & 7));
+                            for (int y = 0; y < 8; ++y) {
+                                const uint32_t e = (w[y >> 1] >> (16 * (y & 1))) & Elem<T>::kExpMask;
+                                if (e == Elem<T>::kExpMask) {
+                                    w[y >> 1] &= y & 1 ? 0xFFFFu : 0xFFFF0000u;
+                                    atomicMin(const_cast<int*>(badc) + bad_now + col + y, r);
+                                }
+                            }
+                            any_bad[c & 1] = 1;
+                            sts128(sV + 16u * x, make_uint4(w[0], w[1], w[2], w[3]));
+                            changed = true;
+                        }
+                    }
+                }
+                if (changed) fence_proxy_async_smem();
+            }
+
+            float rowf = 1.f;
+            if (OUT) {
+                // Scores with their decays.
+                wait(qkdone, c);
+                tc_fence_after();
+                float p[2][32];
+                tc_ld32(tmem + lanes + kColA + 64u * hc, p[0]);
+                tc_ld32(tmem + lanes + kColA + 64u * hc + 32u, p[1]);
+                tc_wait_ld(p[0]);
+                tc_wait_ld(p[1]);
+                const float bh = dec[row], bl = dec[C + row];
+                float m = 0.f;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const float4 h4 = *reinterpret_cast<const float4*>(dec + 64 * hc + 4 * x);
+                    const float4 l4 = *reinterpret_cast<const float4*>(dec + C + 64 * hc + 4 * x);
+                    const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        float d = (bh - hj[y]) + (bl - lj[y]);
+                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(d));
+                        float& v = p[x >> 3][4 * (x & 7) + y];
+                        v = 64 * hc + 4 * x + y <= row ? v * d : 0.f;
+                        m = fmaxf(m, fabsf(v));
+                    }
+                }
+                float tp = 1.f;
+                if (kHalf16) sy[128 * hc + row] = m;
+                bar_first256();                          // both halves of a row are read: the operand may go there
+                if (kHalf16) {
+                    m = fmaxf(m, sy[128 * (hc ^ 1) + row]);
+                    const int e = (__float_as_int(m) >> 23) - 127;
+                    const int rs = m == 0.f || e > 127 ? 0 : max(-126, min(126, 14 - e));
+                    tp = exp2i(rs);
+                    rowf = exp2i(-rs);
+                }
+                uint32_t w[32];
+#pragma unroll
+                for (int y = 0; y < 32; ++y)
+                    w[y] = Elem<T>::pack(p[y >> 4][2 * (y & 15)] * tp, p[y >> 4][2 * (y & 15) + 1] * tp);
+                tc_st32(tmem + lanes + kColA + 32u * hc, w);
+                tc_wait_st();
+                tc_fence_before();
+                tell(pready);
+                if (!kHalf16) wait(qfree, c);            // Q's place is the third part's
+            }
+
+            // The decayed keys in parts, the first in the keys' own place.
+            {
+                const float pk = exp2i(sk);
+#pragma unroll 2
+                for (int x = tid; x < (int)KB / 16; x += 256) {
+                    const int r = (x >> 3) & 127;
+                    const float w = dec[3 * C + r] * pk;
+                    const uint4 kv = lds128(k + 16u * x);
+                    const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w};
+                    uint32_t p0[4], p1[4], p2[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        float2 f = Elem<T>::unpack(kw[y]);
+                        f.x = r < n ? f.x * w : 0.f;
+                        f.y = r < n ? f.y * w : 0.f;
+                        p0[y] = Elem<T>::pack(f.x, f.y);
+                        const float2 u = Elem<T>::unpack(p0[y]);
+                        f.x -= u.x;
+                        f.y -= u.y;
+                        p1[y] = Elem<T>::pack(f.x, f.y);
+                        if (!kHalf16) {
+                            const float2 v = Elem<T>::unpack(p1[y]);
+                            p2[y] = Elem<T>::pack(f.x - v.x, f.y - v.y);
+                        }
+                    }
+                    sts128(k + 16u * x, make_uint4(p0[0], p0[1], p0[2], p0[3]));
+                    sts128(sX + 16u * x, make_uint4(p1[0], p1[1], p1[2], p1[3]));
+                    if (!kHalf16) sts128(sQ + 16u * x, make_uint4(p2[0], p2[1], p2[2], p2[3]));
+                }
+                fence_proxy_async_smem();
+                tell(kready);
+            }
+
+            if (OUT) {
+                // Outputs.
+                const float eb = dec[2 * C + row] * a.scale;
+                rowf *= a.scale;
+                wait(odone, c);
+                tc_fence_after();
+                const bool bad = any_bad[c & 1] != 0;
+                T* out = ob + (t + row) * a.o_stride;
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
+                    float vi[32], vo[32];
+                    tc_ld32(tmem + lanes + kColI + 64u * hc + 32u * x, vi);
+                    tc_ld32(tmem + lanes + kColO + 64u * hc + 32u * x, vo);
+                    tc_wait_ld(vi);
+                    tc_wait_ld(vo);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        float v[8];
+                        const float4 f0 = *reinterpret_cast<const float4*>(colf + 64 * hc + 32 * x + 8 * y);
+                        const float4 f1o = *reinterpret_cast<const float4*>(colf + 64 * hc + 32 * x + 8 * y + 4);
+                        const float cf[8] = {f0.x, f0.y, f0.z, f0.w, f1o.x, f1o.y, f1o.z, f1o.w};
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) {
+                            v[z] = vi[8 * y + z] * cf[z] * eb + vo[8 * y + z] * rowf;
+                            if (bad && badc[bad_now + 64 * hc + 32 * x + 8 * y + z] <= row) v[z] = __int_as_float(0x7FFFFFFF);
+                        }
+                        if (row < n && c0 + 64 * hc + 32 * x + 8 * y < a.v_dim)
+                            *reinterpret_cast<uint4*>(out + 32 * x + 8 * y) = pack8<T>(v);
+                    }
+                }
+                tc_fence_before();
+                tell(oread);
+            }
+            tell(dfree + (c & 1));
+        }
+
+        // The last state.
+        if (ok && nc > 0 && to) {
+            wait(kvdone, nc - 1);
+            tc_fence_after();
+            const bool spoilt = any_bad[(nc - 1) & 1] && badc[128 * ((nc - 1) & 1) + row] < C;
+            const float un = exp2i(-E);
+#pragma unroll 1
+            for (int x = 0; x < CW; x += 32) {
+                float v[32];
+                tc_ld32(tS + x, v);
+                tc_wait_ld(v);
+#pragma unroll
+                for (int y = 0; y < 32; ++y) {
+                    const int dk = hc * CW + x + y;
+                    if (real && dk < a.k_dim) to[(int64_t)dk * a.v_dim] = spoilt ? __int_as_float(0x7FFFFFFF) : v[y] * un;
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace q4

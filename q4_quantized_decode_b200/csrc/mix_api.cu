@@ -12,6 +12,7 @@
 #include "ctx_view.h"
 #include "kv_append.cuh"
 #include "lin_chunk.cuh"
+#include "lin_tc.cuh"
 
 namespace {
 
@@ -151,9 +152,10 @@ cudaError_t split_setup() {
                                 q4::split_smem(DP));
 }
 
-// Tensor map of one half of a paged cache for boxes of 64 elements x `box`
-// tokens in the 128-byte swizzle; false where the driver refuses it.
-bool page_map(CUtensorMap* map, void* base, const q4gemv_kv& c, int box) {
+// Tensor map of 16-bit elements in the 128-byte swizzle, boxes of 64 elements;
+// false where the driver refuses it.
+bool tensor_map(CUtensorMap* map, const void* base, int dtype, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                const cuuint32_t* box) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -168,14 +170,29 @@ bool page_map(CUtensorMap* map, void* base, const q4gemv_kv& c, int box) {
         return reinterpret_cast<Encode>(f);
     }();
     if (!encode) return false;
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return encode(map, dtype == Q4GEMV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One half of a paged cache, boxes of `box` tokens.
+bool page_map(CUtensorMap* map, void* base, const q4gemv_kv& c, int box) {
     const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.n_heads,
                                 (cuuint64_t)c.n_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, (cuuint64_t)c.head_stride * 2,
                                    (cuuint64_t)c.page_stride * 2};
-    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
-    return encode(map, c.dtype == Q4GEMV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                  base, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t b[4] = {64, (cuuint32_t)box, 1, 1};
+    return tensor_map(map, base, c.dtype, 4, dims, strides, b);
+}
+
+// Rows of heads, boxes of a chunk's rows.
+bool row_map(CUtensorMap* map, const void* base, int dtype, int64_t dim, int64_t heads, int64_t rows, int64_t stride) {
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t b[3] = {64, 1, (cuuint32_t)q4::kLtTokens};
+    return tensor_map(map, base, dtype, 3, dims, strides, b);
 }
 
 template <typename T>
@@ -189,19 +206,20 @@ cudaError_t tc_setup() {
     return cudaFuncSetAttribute(q4::attn_tc_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, q4::ta_smem(DP));
 }
 
-template <typename T, int DK, int NW>
-cudaError_t chunk_setup() {
-    const cudaError_t e = cudaFuncSetAttribute(q4::lin_chunk_kernel<T, DK, NW, true>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, q4::lc_smem(DK, NW, true));
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(q4::lin_chunk_kernel<T, DK, NW, false>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       q4::lc_smem(DK, NW, false));
+template <typename F>
+cudaError_t smem_limit(F* kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 template <typename T>
 cudaError_t setup_type() {
-    for (cudaError_t e : {split_setup<T, 64>(), split_setup<T, 128>(), split_setup<T, 256>(), tc_setup<T, 64>(),
-                          tc_setup<T, 128>(), chunk_setup<T, 64, 4>(), chunk_setup<T, 64, 8>(),
-                          chunk_setup<T, 128, 4>(), chunk_setup<T, 128, 8>(), chunk_setup<T, 256, 4>()})
+    for (cudaError_t e :
+         {split_setup<T, 64>(), split_setup<T, 128>(), split_setup<T, 256>(), tc_setup<T, 64>(), tc_setup<T, 128>(),
+          smem_limit(q4::lin_chunk_kernel<T, 256, 4, true>, q4::lc_smem(256, 4, true)),
+          smem_limit(q4::lin_chunk_kernel<T, 256, 4, false>, q4::lc_smem(256, 4, false)),
+          smem_limit(q4::lin_tc_kernel<T, 64, true>, q4::lt_smem(64, true)),
+          smem_limit(q4::lin_tc_kernel<T, 64, false>, q4::lt_smem(64, false)),
+          smem_limit(q4::lin_tc_kernel<T, 128, true>, q4::lt_smem(128, true)),
+          smem_limit(q4::lin_tc_kernel<T, 128, false>, q4::lt_smem(128, false))})
         if (e != cudaSuccess) return e;
     return cudaSuccess;
 }
@@ -401,38 +419,48 @@ cudaError_t lin_recur_launch(const q4::LinArgs& a, cudaStream_t st) {
     return launch(q4::lin_recur_kernel<T, 16>, grid, q4::kLinThreads, 0, st, a);
 }
 
-template <typename T, int DK, int NW, bool OUT>
-cudaError_t lin_chunk_launch(const q4::LinSegArgs& g, cudaStream_t st) {
-    const dim3 grid((unsigned)g.a.v_heads, (unsigned)((g.a.v_dim + q4::lc_cols(NW) - 1) / q4::lc_cols(NW)),
-                    (unsigned)(g.a.n_seqs * g.segs));
-    return launch(q4::lin_chunk_kernel<T, DK, NW, OUT>, grid, 32 * (NW + 1), q4::lc_smem(DK, NW, OUT), st, g);
-}
 template <typename T, bool OUT>
-cudaError_t lin_chunks(const q4::LinSegArgs& g, cudaStream_t st) {
-    const bool wide = g.a.v_dim > 64;
-    if (g.a.k_dim <= 64) return wide ? lin_chunk_launch<T, 64, 8, OUT>(g, st) : lin_chunk_launch<T, 64, 4, OUT>(g, st);
-    if (g.a.k_dim <= 128) return wide ? lin_chunk_launch<T, 128, 8, OUT>(g, st) : lin_chunk_launch<T, 128, 4, OUT>(g, st);
-    return lin_chunk_launch<T, 256, 4, OUT>(g, st);
+cudaError_t lin_chunks(const q4::LinTcArgs& ta, cudaStream_t st) {
+    const q4::LinSegArgs& g = ta.g;
+    const unsigned z = (unsigned)(g.a.n_seqs * g.segs), y = (unsigned)((g.a.v_dim + 127) / 128);
+    if (g.tokens != q4::kLtTokens)
+        return launch(q4::lin_chunk_kernel<T, 256, 4, OUT>, dim3((unsigned)g.a.v_heads, (unsigned)((g.a.v_dim + 63) / 64), z),
+                      64 * 4, q4::lc_smem(256, 4, OUT), st, g);
+    const dim3 grid((unsigned)g.a.v_heads, y, z);
+    return g.a.k_dim <= 64 ? launch(q4::lin_tc_kernel<T, 64, OUT>, grid, q4::kLtThreads, q4::lt_smem(64, OUT), st, ta)
+                           : launch(q4::lin_tc_kernel<T, 128, OUT>, grid, q4::kLtThreads, q4::lt_smem(128, OUT), st, ta);
 }
 
 // Prompts run in chunks, cut into segments where sequences and heads alone
 // would leave SMs idle (a segment costs half as much again: its gain is
 // computed first).
 template <typename T>
-cudaError_t lin_prompt_launch(const q4::LinArgs& a, int64_t max_new, const q4::CtxView& cx, cudaStream_t st) {
-    q4::LinSegArgs g;
+cudaError_t lin_prompt_launch(const q4::LinArgs& a, int64_t qk_heads, int dtype, int64_t max_new, const q4::CtxView& cx,
+                              cudaStream_t st) {
+    q4::LinTcArgs ta;
+    q4::LinSegArgs& g = ta.g;
     g.a = a;
     g.ws = cx.attn_ws;
-    const int64_t slices = a.k_dim > 128 || a.v_dim <= 64 ? (a.v_dim + 63) / 64 : (a.v_dim + 127) / 128;
+    const bool bf16 = dtype == Q4GEMV_BF16;
+    ta.idesc_a = ta.idesc_i = q4::tc_idesc_16(128, 128, bf16, false);
+    ta.idesc_o = q4::tc_idesc_16(128, 128, bf16, true);
+    ta.idesc_s = q4::tc_idesc_16(128, a.k_dim <= 64 ? 64 : 128, bf16, true) | q4::kTcAMmajor;
+    // The tcgen05 kernel holds states of up to 128 x 128; it reads whole boxes
+    // of rows by tensor map.
+    const bool tc = a.k_dim <= 128 && a.rows > 0 &&
+                    row_map(&ta.qmap, a.q, dtype, a.k_dim, qk_heads, a.rows, a.q_stride) &&
+                    row_map(&ta.kmap, a.k, dtype, a.k_dim, qk_heads, a.rows, a.k_stride) &&
+                    row_map(&ta.vmap, a.v, dtype, a.v_dim, a.v_heads, a.rows, a.v_stride);
+    g.tokens = tc ? q4::kLtTokens : q4::kLcTokens;
+    const int64_t slices = tc ? (a.v_dim + 127) / 128 : (a.v_dim + 63) / 64;
     const int64_t ctas = (int64_t)a.n_seqs * a.v_heads * slices;
-    const int64_t chunks = (std::min(max_new, a.rows) + q4::kLcTokens - 1) / q4::kLcTokens;
+    const int64_t chunks = (std::min(max_new, a.rows) + g.tokens - 1) / g.tokens;
     const int64_t room = (int64_t)(cx.attn_ws_bytes / sizeof(float)) /
                          ((int64_t)a.n_seqs * a.v_heads * ((int64_t)a.k_dim * a.v_dim + 1));
-    int64_t segs = std::min<int64_t>({cx.sms / ctas, chunks / kLinSegChunks, room, 65535 / a.n_seqs});
-    g.segs = (int)std::max<int64_t>(segs, 1);
-    if (g.segs < 3) g.segs = 1;
+    const int64_t segs = std::min<int64_t>({cx.sms / ctas, chunks / kLinSegChunks, room, 65535 / a.n_seqs});
+    g.segs = segs < 3 ? 1 : (int)segs;
     if (g.segs > 1) {
-        cudaError_t e = lin_chunks<T, false>(g, st);
+        cudaError_t e = lin_chunks<T, false>(ta, st);
         if (e != cudaSuccess) return e;
         const int64_t size = (int64_t)a.k_dim * a.v_dim;
         e = launch(q4::lin_scan_kernel, dim3((unsigned)((size / 4 + q4::kLinScanThreads - 1) / q4::kLinScanThreads),
@@ -440,7 +468,7 @@ cudaError_t lin_prompt_launch(const q4::LinArgs& a, int64_t max_new, const q4::C
                    q4::kLinScanThreads, 0, st, g);
         if (e != cudaSuccess) return e;
     }
-    return lin_chunks<T, true>(g, st);
+    return lin_chunks<T, true>(ta, st);
 }
 
 }  // namespace
@@ -506,6 +534,6 @@ extern "C" int q4gemv_linattn(q4gemv_t h, const q4gemv_linattn_args* args, int64
     const bool f16 = p.dtype == Q4GEMV_F16;
     if (max_new <= kLinRecurMax)
         return launch_status(h, f16 ? lin_recur_launch<__half>(a, st) : lin_recur_launch<__nv_bfloat16>(a, st), call);
-    return launch_status(h, f16 ? lin_prompt_launch<__half>(a, max_new, cx, st)
-                                : lin_prompt_launch<__nv_bfloat16>(a, max_new, cx, st), call);
+    return launch_status(h, f16 ? lin_prompt_launch<__half>(a, p.qk_heads, p.dtype, max_new, cx, st)
+                                : lin_prompt_launch<__nv_bfloat16>(a, p.qk_heads, p.dtype, max_new, cx, st), call);
 }

@@ -33,7 +33,9 @@ __host__ __device__ constexpr uint64_t tc_sdesc_sw128(uint32_t saddr) {
 __host__ __device__ constexpr uint32_t tc_idesc_16(int m, int n, bool bf16, bool b_nmajor) {
     return tc_idesc_f16(m, n) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_nmajor ? 1u << 16 : 0u);
 }
-// Shared-memory matrix descriptor of an N-major, 128-byte-swizzled B operand: a
+// A read from a [K][M] tile (M-major).
+constexpr uint32_t kTcAMmajor = 1u << 15;
+// Shared-memory matrix descriptor of an N-major, 128-byte-swizzled B operand (or M-major A): a
 // [K][64] tile of 128-byte rows (8-row groups 1024 bytes apart) for every 64
 // columns of N, the tiles `n_step` bytes apart.
 __host__ __device__ constexpr uint64_t tc_sdesc_sw128_nmajor(uint32_t saddr, uint32_t n_step) {
@@ -168,6 +170,31 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&v)[32])
                    "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
                    "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
                  : "memory");
+}
+
+// A wait that gives up when another role has, or after about 20 seconds (the
+// longest that a role keeps others waiting in earnest is attention taken row by
+// row, milliseconds for ordinary contexts).
+__device__ __forceinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 15) == 15 && (*abort_flag || clock64() - t0 > (1ll << 35))) return false;
+    }
+}
+
+// Barrier 1 of a CTA's first 256 threads.
+__device__ __forceinline__ void bar_first256() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The same; whether `ok` holds for all of them.
+__device__ __forceinline__ bool all_first256(bool ok) {
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.cta.red.and.pred q, 1, 256, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all) : "r"((uint32_t)ok) : "memory");
+    return all != 0;
 }
 
 }  // namespace q4

@@ -14,8 +14,11 @@ Tolerances, from the arithmetic (u = half a step of the 16-bit type):
           weighted magnitudes of v (2^-18: exp2 and the sums of up to 2^11
           steps of 2^-23 in tiles).
   linear  state: 32-bit sums of a token's terms, at most (tokens + 64) 2^-22 of
-          their magnitudes; out: operands of the products may be rounded to
-          11 bits once each (2 * 2^-11), plus the same, plus u |o|.
+          their magnitudes.  out: each term (state times query, or score times
+          value) has one operand that is rounded once to the type, a factor
+          1 + d with |d| <= u: together at most u A, A the terms' magnitudes
+          (binary16 is given 2^-10 = 2 u, as before the operands' type was the
+          tensors'; bfloat16 u = 2^-8); the same sums, and u |o| for the output.
 """
 import pytest
 
@@ -491,7 +494,7 @@ class LinearCase:
                                          torch.zeros_like(s0) if zero else s0, scale)
                 sums = (n + 64) * 2.0 ** -22
                 close(state[self.slots[s], h], S, sums * A, f"state {s}, head {h}")
-                close(out[sl, h], o, (2.0 ** -10 + sums) * ao + u * o.abs() + ref.tiny(self.dtype),
+                close(out[sl, h], o, (max(u, 2.0 ** -10) + sums) * ao + u * o.abs() + ref.tiny(self.dtype),
                       f"sequence {s}, head {h}")
 
 
@@ -516,6 +519,41 @@ def test_linear_prompts(eng, dtype, fixed, new, hk, hv, dk, dv):
     out, state = c.run(eng)
     assert eng.sync_status() == q4.Q4_OK
     c.check(out, state)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new", [[1500], [1024, 0, 70, 801], [777, 64]])
+@pytest.mark.parametrize("hk,hv,dk,dv", [(1, 2, 128, 128), (1, 1, 64, 64), (1, 1, 256, 72)])
+def test_linear_long_prompts_in_segments(eng, dtype, new, hk, hv, dk, dv):
+    """Few heads and long prompts: sequences run as parallel segments, some of
+    them without tokens; the state is updated in place."""
+    c = LinearCase(new, hk, hv, dk, dv, dtype, seed=sum(new) + dv, rate=(-4.0, -12.0))
+    state = c.state.to(DEV)
+    out, end = c.run(eng, state=state)
+    assert end is state and eng.sync_status() == q4.Q4_OK
+    c.check(out, state)
+    zero = torch.full_like(state, 9.0)
+    out, _ = eng.linattn(c.gq, c.gk, c.gv, c.gg, c.start, None, state_out=zero, slots=c.slots.to(DEV), max_new=max(new))
+    c.check(out, zero, zero=True)
+    again, _ = c.run(eng, max_new=1 << 20)               # another cut
+    c.check(again, c.run(eng, max_new=64)[1])
+
+
+def test_linear_segments_pass_non_finite_states_on(eng):
+    c = LinearCase([1400], 1, 2, 64, 64, torch.float16, seed=30)
+    out0, _ = c.run(eng)
+    c.gv = c.gv.clone()
+    c.gv[700, 0, 5] = float("nan")
+    out, state = c.run(eng)
+    assert eng.sync_status() == q4.Q4_OK
+    mixed = out0.clone()
+    mixed[:700] = out[:700]
+    mixed[:, 1] = out[:, 1]
+    mixed[:, 0, :5] = out[:, 0, :5]
+    ref_state = c.run(eng)[1].clone()
+    assert torch.isnan(out[700:, 0, 5]).all() and torch.isnan(ref_state[c.slots[0], 0, :, 5]).all()
+    clean = LinearCase([1400], 1, 2, 64, 64, torch.float16, seed=30)
+    clean.check(mixed, clean.run(eng)[1])
 
 
 @pytest.mark.parametrize("rate", [(3.0, 7.0), (-14.0, -20.0)])
