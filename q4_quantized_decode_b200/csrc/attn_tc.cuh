@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
             // The eight warps go on, or end, together.
             if (!told_part()) ok = false;
             if (!ok) give_up();
-            if (!all_first256(ok)) break;
+            if (!all_of<256>(ok)) break;
             const TaSeg& e = segs[part_no % kTaSegs];
             if (!e.more) break;
             const int xr = acc * 128 + row;              // of the unit's rows

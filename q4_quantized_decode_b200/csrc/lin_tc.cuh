@@ -6,14 +6,14 @@
 // a chunk is four products with all accumulators in tensor memory: the scores
 // Q K^T, the part of the outputs from the state, the part from the chunk, and
 // what the state gains (the state stays there, as S^T: a value column a lane).
-//   warps 0-7  the passes between the products, a thread half a row: the state
+//   warps 0-15 the passes between the products, a thread a quarter row: the state
 //              to a 16-bit operand in shared memory and times its decay in
 //              place; the scores times their decays, to the 16-bit operand in
 //              their own place; the decayed keys k' = e^{b_C - b_j} k_j split
 //              into 16-bit parts; values looked over; outputs out
-//   warp 8     one thread issues the products
-//   warp 9     one thread loads Q, K and V by tensor map, K a chunk ahead
-//   warp 10    sums of the log decays, a chunk ahead
+//   warp 16    one thread issues the products
+//   warp 17    one thread loads Q, K and V by tensor map, K a chunk ahead
+//   warp 18    sums of the log decays, a chunk ahead
 // What bounds it: the passes, about 5 instructions for each of 5 x 16384 values
 // of a chunk, twice the 2560 cycles of the products.
 //
@@ -40,15 +40,18 @@
 namespace q4 {
 
 constexpr int kLtTokens = 128;
-constexpr int kLtThreads = 32 * 12;
+constexpr int kLtPass = 512;                         // threads of the passes
+constexpr int kLtParts = kLtPass / kLtTokens;        // threads of a row
+constexpr int kLtThreads = kLtPass + 32 * 4;
 constexpr uint32_t kLtHalf = kLtTokens * 128;        // [128 rows][64 elements]
 constexpr int kLtDec = 4 * kLtTokens + 4;            // floats of a chunk's decays
 
 __host__ __device__ constexpr int lt_kbytes(int dk) { return kLtTokens * dk * 2; }
-// Q, two K's, V, the keys' second part, the state's operand.
+// Two K's, the keys' second part, V, Q (or their third part), the state's operand,
+// in whose place the outputs are laid in rows.
 __host__ __device__ constexpr int lt_smem(int dk, bool out) {
-    return 1024 + (out ? 2 : 0) * lt_kbytes(dk) + 3 * lt_kbytes(dk) + 2 * (int)kLtHalf + (out ? 0 : lt_kbytes(dk)) +
-           2 * kLtDec * 4 + (4 * 128 + 128 + 2 * 128 + 16) * 4 + 256;
+    return 1024 + 4 * lt_kbytes(dk) + (out ? 4 : 2) * (int)kLtHalf + 2 * kLtDec * 4 +
+           (2 * kLtParts * 128 + 128 + 2 * 128 + 32) * 4 + 256;
 }
 
 struct LinTcArgs {
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     constexpr bool kHalf16 = Elem<T>::kExpMask == Elem<__half>::kExpMask;
     constexpr int C = kLtTokens;
     constexpr uint32_t KB = lt_kbytes(DK);
-    constexpr int CW = DK / 2;                           // state columns of a thread
+    constexpr int CW = DK / kLtParts;                    // state columns of a thread: 32 or 16
     constexpr uint32_t kColA = 128, kColI = 256, kColO = 384;   // TMEM: state at 0, scores, outputs' two parts
     extern __shared__ uint8_t lt_raw[];
     const LinSegArgs& g = ta.g;
@@ -118,17 +121,17 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     const uint32_t sV = sX + KB;
     const uint32_t sQ = sV + 2 * kLtHalf;                // with OUT; the third part (bfloat16) in its place, or after V
     const uint32_t sS = sQ + KB;                         // the state's operand, with OUT
-    float* fl = reinterpret_cast<float*>(lt_raw + ((OUT ? sS + KB : sQ + KB) - raw0));
-    float* sx = fl + 2 * kLtDec;                         // [2][128] row maxima of the halves: state, scores
-    float* sy = sx + 256;
-    float* colf = sy + 256;                              // [128] scale of a value column of the state's operand
+    float* fl = reinterpret_cast<float*>(lt_raw + (sS + (OUT ? 2 * kLtHalf : 0) - raw0));
+    float* sx = fl + 2 * kLtDec;                         // [parts][128] row maxima: state, scores
+    float* sy = sx + kLtParts * 128;
+    float* colf = sy + kLtParts * 128;                              // [128] scale of a value column of the state's operand
     volatile int* badc = reinterpret_cast<volatile int*>(colf + 128);   // [2][128] first token with a bad value, or 128
-    uint32_t* sMax = reinterpret_cast<uint32_t*>(colf + 384);           // [8] largest |k|
-    volatile int* any_bad = reinterpret_cast<volatile int*>(sMax + 8);  // [2]
+    uint32_t* sMax = reinterpret_cast<uint32_t*>(colf + 384);           // [16] largest |k|
+    volatile int* any_bad = reinterpret_cast<volatile int*>(sMax + 16); // [2]
     volatile int* abort_flag = any_bad + 2;
     volatile int* never = any_bad + 3;
-    uint32_t* tslot = sMax + 12;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sMax + 16);
+    uint32_t* tslot = sMax + 20;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sMax + 32);
     uint64_t *kfull = bars, *qfull = bars + 2, *vfull = bars + 3, *dfull = bars + 4, *dfree = bars + 6, *qkdone = bars + 8,
              *qfree = bars + 9, *odone = bars + 10, *kvdone = bars + 11, *sready = bars + 12, *pready = bars + 13,
              *kready = bars + 14, *oread = bars + 15, *idle = bars + 16;
@@ -138,16 +141,16 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         for (int i = 0; i < 2; ++i) {
             mbar_init(kfull + i, 1);
             mbar_init(dfull + i, 1);
-            mbar_init(dfree + i, 8);
+            mbar_init(dfree + i, kLtPass / 32);
             any_bad[i] = 0;
         }
         for (uint64_t* b : {qfull, vfull, qkdone, qfree, odone, kvdone, idle}) mbar_init(b, 1);
-        for (uint64_t* b : {sready, pready, kready, oread}) mbar_init(b, 8);
+        for (uint64_t* b : {sready, pready, kready, oread}) mbar_init(b, kLtPass / 32);
         *abort_flag = *never = 0;
         fence_barrier_init();
     }
     if (threadIdx.x < 256) badc[threadIdx.x] = C;
-    if (warp == 8) tc_alloc(tslot, 512);
+    if (warp == 16) tc_alloc(tslot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         set_device_error(a.err, kDevTimeout);
     };
 
-    if (warp == 9) {
+    if (warp == 17) {
         // ---- loads ----
         if (lane == 0) {
             bool ok = true;
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             if (nv > 0) tc_wait_long(vfull, (nv - 1) & 1, never);
         }
         __syncwarp();
-    } else if (warp == 10) {
+    } else if (warp == 18) {
         // ---- decays ----
         double total = 0;
         bool ok = true;
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         }
         if (!ok) give_up();
         if (!OUT && work && lane == 0 && blockIdx.y == 0) *seg_decay(g, s, h, seg) = expf((float)total);
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // ---- products ----
         if (lane == 0) {
             bool ok = true;
@@ -292,8 +295,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             tc_wait_long(idle, 0, never);
         }
         __syncwarp();
-    } else if (warp < 8 && work) {
-        // ---- passes: lane quadrant warp % 4, column half warp / 4 ----
+    } else if (warp < 16 && work) {
+        // ---- passes: lane quadrant warp % 4, column part warp / 4 ----
         const int row = 32 * (warp & 3) + lane, hc = warp >> 2, tid = threadIdx.x;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + (uint32_t)(hc * CW);
@@ -303,19 +306,28 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         float* to = OUT ? (last ? a.state_out + so : nullptr) : seg_state(g, s, h, seg);
         if (from) from += c0 + row;
         if (to) to += c0 + row;
+        auto load_state = [&](uint32_t (&v)[CW]) {
+            if constexpr (CW == 32) tc_ld32(tS, reinterpret_cast<float(&)[32]>(v));
+            else tc_ld16(tS, v);
+            if constexpr (CW == 32) tc_wait_ld(reinterpret_cast<float(&)[32]>(v));
+        };
+        auto store_state = [&](const uint32_t (&v)[CW]) {
+            if constexpr (CW == 32) tc_st32(tS, v);
+            else tc_st16(tS, v);
+            tc_wait_st();
+        };
         // The first state.
-#pragma unroll 1
-        for (int x = 0; x < CW; x += 32) {
-            uint32_t v[32];
+        {
+            uint32_t v[CW];
 #pragma unroll
-            for (int y = 0; y < 32; ++y) {
-                const int dk = hc * CW + x + y;
-                v[y] = from && real && dk < a.k_dim ? __float_as_uint(from[(int64_t)dk * a.v_dim]) : 0u;
-                if (nc == 0 && to && real && dk < a.k_dim) to[(int64_t)dk * a.v_dim] = __uint_as_float(v[y]);
-            }
-            tc_st32(tS + x, v);
+            for (int y = 0; y < CW; ++y)
+                v[y] = from && real && hc * CW + y < a.k_dim ? __float_as_uint(from[(int64_t)(hc * CW + y) * a.v_dim]) : 0u;
+            store_state(v);
+            if (nc == 0 && to && real)
+#pragma unroll
+                for (int y = 0; y < CW; ++y)
+                    if (hc * CW + y < a.k_dim) to[(int64_t)(hc * CW + y) * a.v_dim] = __uint_as_float(v[y]);
         }
-        tc_wait_st();
         int E = 0;                                       // TMEM holds the state times 2^E
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t par) {
@@ -327,7 +339,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        T* ob = static_cast<T*>(a.out) + (int64_t)h * a.v_dim + c0 + 64 * hc;
+        T* ob = static_cast<T*>(a.out) + (int64_t)h * a.v_dim + c0;
+        auto bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kLtPass) : "memory"); };
         for (int c = 0; c < nc; ++c) {
             const int64_t t = t0 + (int64_t)c * C;
             const int n = (int)min((int64_t)C, t1 - t);
@@ -340,18 +353,18 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             if (kHalf16) {
                 uint32_t m = 0;
 #pragma unroll 4
-                for (int x = tid; x < (int)KB / 16; x += 256)
+                for (int x = tid; x < (int)KB / 16; x += kLtPass)
                     if (((x >> 3) & 127) < n) m = max_abs8(m, lds128(k + 16u * x));
                 for (int x = 16; x; x >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
                 if (lane == 0) sMax[warp] = m;
             }
             wait(dfull + (c & 1), c >> 1);
-            if (!all_first256(ok)) break;
+            if (!all_of<kLtPass>(ok)) break;
             int sk = 0;
             if (kHalf16) {
                 uint32_t m = sMax[0];
 #pragma unroll
-                for (int y = 1; y < 8; ++y) m = __vmaxu2(m, sMax[y]);
+                for (int y = 1; y < kLtPass / 32; ++y) m = __vmaxu2(m, sMax[y]);
                 const uint32_t top = max(m & 0xFFFFu, m >> 16);
                 // The largest to [2^14, 2^15); with infinities or NaN, what suits any finite key.
                 sk = top >= Elem<__half>::kExpMask ? -2
@@ -364,34 +377,28 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             const bool spoilt = any_bad[(c & 1) ^ 1] && badc[bad_then + row] < C;   // by the last chunk's values
             const float decay = dec[4 * C], f1 = exp2i(sk - E);
             float rp = 1.f;
-            float sv[CW / 32][32];
-#pragma unroll
-            for (int x = 0; x < CW / 32; ++x) tc_ld32(tS + 32u * x, sv[x]);
-#pragma unroll
-            for (int x = 0; x < CW / 32; ++x) tc_wait_ld(sv[x]);
+            uint32_t sv[CW];
+            load_state(sv);
             if (spoilt)
 #pragma unroll
-                for (int x = 0; x < CW / 32; ++x)
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) sv[x][y] = __int_as_float(0x7FFFFFFF);
+                for (int y = 0; y < CW; ++y) sv[y] = 0x7FFFFFFFu;
             if (OUT && kHalf16) {
                 float m = 0.f;
 #pragma unroll
-                for (int x = 0; x < CW / 32; ++x)
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) m = fmaxf(m, fabsf(sv[x][y]));
+                for (int y = 0; y < CW; ++y) m = fmaxf(m, fabsf(__uint_as_float(sv[y])));
                 sx[128 * hc + row] = m;
-                bar_first256();
-                m = fmaxf(m, sx[128 * (hc ^ 1) + row]);
+            }
+            bar();
+            if (OUT && kHalf16) {
+                float m = sx[row];
+#pragma unroll
+                for (int y = 1; y < kLtParts; ++y) m = fmaxf(m, sx[128 * y + row]);
                 const int e = (__float_as_int(m) >> 23) - 127;
                 const int rs = m == 0.f || e > 127 ? 0 : min(126, 14 - e);
                 rp = exp2i(rs);
                 if (hc == 0) colf[row] = exp2i(-rs - E);
-            } else if (OUT) {
-                if (hc == 0) colf[row] = 1.f;
-                bar_first256();
-            } else {
-                bar_first256();
+            } else if (OUT && hc == 0) {
+                colf[row] = 1.f;
             }
             if (hc == 0 && spoilt) badc[bad_then + row] = C;
             if (tid == 0) any_bad[(c & 1) ^ 1] = 0;
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                 for (int x = 0; x < CW / 8; ++x) {
                     float v[8];
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) v[y] = sv[x / 4][8 * (x % 4) + y] * rp;
+                    for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(sv[8 * x + y]) * rp;
                     const int ch = hc * (CW / 8) + x;    // 16-byte chunk of the row
                     sts128(sS + (uint32_t)(ch >> 3) * kLtHalf + (uint32_t)(row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
                            pack8<T>(v));
@@ -408,13 +415,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                 fence_proxy_async_smem();
             }
 #pragma unroll
-            for (int x = 0; x < CW / 32; ++x) {
-                uint32_t v[32];
-#pragma unroll
-                for (int y = 0; y < 32; ++y) v[y] = __float_as_uint(sv[x][y] * decay * f1);
-                tc_st32(tS + 32u * x, v);
-            }
-            tc_wait_st();
+            for (int y = 0; y < CW; ++y) sv[y] = __float_as_uint(__uint_as_float(sv[y]) * decay * f1);
+            store_state(sv);
             tc_fence_before();
             E = sk;
             tell(sready);
@@ -423,32 +425,31 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             // are not finite, which are remembered.
             wait(vfull, c);
             {
-                bool changed = false;
-#pragma unroll 4
-                for (int x = tid; x < (int)(2 * kLtHalf / 16); x += 256) {
-                    const int r = (x >> 3) & 127;
-                    if (r >= n) {
-                        sts128(sV + 16u * x, make_uint4(0, 0, 0, 0));
-                        changed = true;
-                    } else {
+                constexpr int N = (int)(2 * kLtHalf / 16) / kLtPass;
+                bool odd = n < C;
+#pragma unroll
+                for (int x = 0; x < N; ++x) odd |= any_nonfinite<T>(lds128(sV + 16u * (tid + x * kLtPass)));
+                if (odd) {
+                    for (int x = tid; x < (int)(2 * kLtHalf / 16); x += kLtPass) {
+                        const int r = (x >> 3) & 127;
                         const uint4 v = lds128(sV + 16u * x);
-                        if (any_nonfinite<T>(v)) {
-                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        if (r >= n) {
+                            w[0] = w[1] = w[2] = w[3] = 0;
+                        } else if (any_nonfinite<T>(v)) {
                             const int col = 64 * (x >> 10) + 8 * ((x & 7) ^ (r & 7));
-                            for (int y = 0; y < 8; ++y) {
-                                const uint32_t e = (w[y >> 1] >> (16 * (y & 1))) & Elem<T>::kExpMask;
-                                if (e == Elem<T>::kExpMask) {
+#pragma unroll
+                            for (int y = 0; y < 8; ++y)
+                                if (((w[y >> 1] >> (16 * (y & 1))) & Elem<T>::kExpMask) == Elem<T>::kExpMask) {
                                     w[y >> 1] &= y & 1 ? 0xFFFFu : 0xFFFF0000u;
                                     atomicMin(const_cast<int*>(badc) + bad_now + col + y, r);
                                 }
-                            }
                             any_bad[c & 1] = 1;
-                            sts128(sV + 16u * x, make_uint4(w[0], w[1], w[2], w[3]));
-                            changed = true;
                         }
+                        sts128(sV + 16u * x, make_uint4(w[0], w[1], w[2], w[3]));
                     }
+                    fence_proxy_async_smem();
                 }
-                if (changed) fence_proxy_async_smem();
             }
 
             float rowf = 1.f;
@@ -456,42 +457,46 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                 // Scores with their decays.
                 wait(qkdone, c);
                 tc_fence_after();
-                float p[2][32];
-                tc_ld32(tmem + lanes + kColA + 64u * hc, p[0]);
-                tc_ld32(tmem + lanes + kColA + 64u * hc + 32u, p[1]);
-                tc_wait_ld(p[0]);
-                tc_wait_ld(p[1]);
-                const float bh = dec[row], bl = dec[C + row];
+                float p[32];
+                tc_ld32(tmem + lanes + kColA + 32u * hc, p);
+                tc_wait_ld(p);
                 float m = 0.f;
+                if (hc <= (warp & 3)) {                  // else wholly above the diagonal
+                    const float bh = dec[row], bl = dec[C + row];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const float4 h4 = *reinterpret_cast<const float4*>(dec + 64 * hc + 4 * x);
-                    const float4 l4 = *reinterpret_cast<const float4*>(dec + C + 64 * hc + 4 * x);
-                    const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
+                    for (int x = 0; x < 8; ++x) {
+                        const float4 h4 = *reinterpret_cast<const float4*>(dec + 32 * hc + 4 * x);
+                        const float4 l4 = *reinterpret_cast<const float4*>(dec + C + 32 * hc + 4 * x);
+                        const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        float d = (bh - hj[y]) + (bl - lj[y]);
-                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(d));
-                        float& v = p[x >> 3][4 * (x & 7) + y];
-                        v = 64 * hc + 4 * x + y <= row ? v * d : 0.f;
-                        m = fmaxf(m, fabsf(v));
+                        for (int y = 0; y < 4; ++y) {
+                            float d = (bh - hj[y]) + (bl - lj[y]);
+                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(d));
+                            float& v = p[4 * x + y];
+                            v = 32 * hc + 4 * x + y <= row ? v * d : 0.f;
+                            m = fmaxf(m, fabsf(v));
+                        }
                     }
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) p[y] = 0.f;
                 }
                 float tp = 1.f;
                 if (kHalf16) sy[128 * hc + row] = m;
-                bar_first256();                          // both halves of a row are read: the operand may go there
+                bar();                                   // a row's parts are read: the operand may go there
                 if (kHalf16) {
-                    m = fmaxf(m, sy[128 * (hc ^ 1) + row]);
+                    m = sy[row];
+#pragma unroll
+                    for (int y = 1; y < kLtParts; ++y) m = fmaxf(m, sy[128 * y + row]);
                     const int e = (__float_as_int(m) >> 23) - 127;
                     const int rs = m == 0.f || e > 127 ? 0 : max(-126, min(126, 14 - e));
                     tp = exp2i(rs);
                     rowf = exp2i(-rs);
                 }
-                uint32_t w[32];
+                uint32_t w[16];
 #pragma unroll
-                for (int y = 0; y < 32; ++y)
-                    w[y] = Elem<T>::pack(p[y >> 4][2 * (y & 15)] * tp, p[y >> 4][2 * (y & 15) + 1] * tp);
-                tc_st32(tmem + lanes + kColA + 32u * hc, w);
+                for (int y = 0; y < 16; ++y) w[y] = Elem<T>::pack(p[2 * y] * tp, p[2 * y + 1] * tp);
+                tc_st16(tmem + lanes + kColA + 16u * hc, w);
                 tc_wait_st();
                 tc_fence_before();
                 tell(pready);
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             {
                 const float pk = exp2i(sk);
 #pragma unroll 2
-                for (int x = tid; x < (int)KB / 16; x += 256) {
+                for (int x = tid; x < (int)KB / 16; x += kLtPass) {
                     const int r = (x >> 3) & 127;
                     const float w = dec[3 * C + r] * pk;
                     const uint4 kv = lds128(k + 16u * x);
@@ -538,31 +543,37 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                 wait(odone, c);
                 tc_fence_after();
                 const bool bad = any_bad[c & 1] != 0;
-                T* out = ob + (t + row) * a.o_stride;
-#pragma unroll 1
-                for (int x = 0; x < 2; ++x) {
+                // Into rows in the state operand's place, then out.
+                {
                     float vi[32], vo[32];
-                    tc_ld32(tmem + lanes + kColI + 64u * hc + 32u * x, vi);
-                    tc_ld32(tmem + lanes + kColO + 64u * hc + 32u * x, vo);
+                    tc_ld32(tmem + lanes + kColI + 32u * hc, vi);
+                    tc_ld32(tmem + lanes + kColO + 32u * hc, vo);
                     tc_wait_ld(vi);
                     tc_wait_ld(vo);
+                    tc_fence_before();
+                    tell(oread);
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         float v[8];
-                        const float4 f0 = *reinterpret_cast<const float4*>(colf + 64 * hc + 32 * x + 8 * y);
-                        const float4 f1o = *reinterpret_cast<const float4*>(colf + 64 * hc + 32 * x + 8 * y + 4);
-                        const float cf[8] = {f0.x, f0.y, f0.z, f0.w, f1o.x, f1o.y, f1o.z, f1o.w};
+                        const float4 f0 = *reinterpret_cast<const float4*>(colf + 32 * hc + 8 * y);
+                        const float4 f4 = *reinterpret_cast<const float4*>(colf + 32 * hc + 8 * y + 4);
+                        const float cf[8] = {f0.x, f0.y, f0.z, f0.w, f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
                         for (int z = 0; z < 8; ++z) {
                             v[z] = vi[8 * y + z] * cf[z] * eb + vo[8 * y + z] * rowf;
-                            if (bad && badc[bad_now + 64 * hc + 32 * x + 8 * y + z] <= row) v[z] = __int_as_float(0x7FFFFFFF);
+                            if (bad && badc[bad_now + 32 * hc + 8 * y + z] <= row) v[z] = __int_as_float(0x7FFFFFFF);
                         }
-                        if (row < n && c0 + 64 * hc + 32 * x + 8 * y < a.v_dim)
-                            *reinterpret_cast<uint4*>(out + 32 * x + 8 * y) = pack8<T>(v);
+                        const int ch = 4 * hc + y;
+                        sts128(sS + (uint32_t)(row * 256 + (((ch & 8) | ((ch ^ row) & 7)) << 4)), pack8<T>(v));
                     }
                 }
-                tc_fence_before();
-                tell(oread);
+                bar();
+#pragma unroll
+                for (int x = 0; x < C * 16 / kLtPass; ++x) {
+                    const int r = (tid >> 4) + x * (kLtPass / 16), ch = tid & 15;
+                    const uint4 v = lds128(sS + (uint32_t)(r * 256 + (((ch & 8) | ((ch ^ r) & 7)) << 4)));
+                    if (r < n && c0 + 8 * ch < a.v_dim) *reinterpret_cast<uint4*>(ob + (t + r) * a.o_stride + 8 * ch) = v;
+                }
             }
             tell(dfree + (c & 1));
         }
@@ -573,23 +584,18 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             tc_fence_after();
             const bool spoilt = any_bad[(nc - 1) & 1] && badc[128 * ((nc - 1) & 1) + row] < C;
             const float un = exp2i(-E);
-#pragma unroll 1
-            for (int x = 0; x < CW; x += 32) {
-                float v[32];
-                tc_ld32(tS + x, v);
-                tc_wait_ld(v);
+            uint32_t v[CW];
+            load_state(v);
 #pragma unroll
-                for (int y = 0; y < 32; ++y) {
-                    const int dk = hc * CW + x + y;
-                    if (real && dk < a.k_dim) to[(int64_t)dk * a.v_dim] = spoilt ? __int_as_float(0x7FFFFFFF) : v[y] * un;
-                }
-            }
+            for (int y = 0; y < CW; ++y)
+                if (real && hc * CW + y < a.k_dim)
+                    to[(int64_t)(hc * CW + y) * a.v_dim] = spoilt ? __int_as_float(0x7FFFFFFF) : __uint_as_float(v[y]) * un;
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc_fence_after();
         tc_dealloc(tmem, 512);
     }

@@ -186,14 +186,15 @@ __device__ __forceinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, vol
 
 // Barrier 1 of a CTA's first 256 threads.
 __device__ __forceinline__ void bar_first256() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-// The same; whether `ok` holds for all of them.
-__device__ __forceinline__ bool all_first256(bool ok) {
+// The same for the first N; whether `ok` holds for all of them.
+template <int N>
+__device__ __forceinline__ bool all_of(bool ok) {
     uint32_t all;
     asm volatile("{\n\t.reg .pred p, q;\n\t"
                  "setp.ne.u32 p, %1, 0;\n\t"
-                 "barrier.cta.red.and.pred q, 1, 256, p;\n\t"
+                 "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
                  "selp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(all) : "r"((uint32_t)ok) : "memory");
+                 : "=r"(all) : "r"((uint32_t)ok), "n"(N) : "memory");
     return all != 0;
 }
 
