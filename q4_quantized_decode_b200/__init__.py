@@ -311,6 +311,7 @@ def _stream(stream) -> int:
 import torch as _torch  # noqa: E402  (after the library: a missing one is reported first)
 
 _raw_stream = _torch._C._cuda_getCurrentRawStream   # current_stream(device).cuda_stream, without the object
+_kv_append, _attn_paged, _linattn = _lib.q4gemv_kv_append, _lib.q4gemv_attn_paged, _lib.q4gemv_linattn
 
 
 def _dtype_code(t) -> int:
@@ -321,25 +322,28 @@ def _dtype_code(t) -> int:
     raise Q4Error(Q4_EINVAL, f"tensor of {t.dtype}: float16 or bfloat16 expected")
 
 
-def _heads(t, name: str, dtype, device, rows=None, heads=None, dim=None):
-    """Row stride of t [rows][heads][dim], its heads and elements packed in a row."""
-    if t.dtype is not dtype or t.device != device:
-        raise Q4Error(Q4_EINVAL, f"{name}: {t.dtype} on {t.device}, {dtype} on {device} expected")
+def _rows(t, name: str, dtype, device):
+    """(rows, heads, dim, row stride) of t [rows][heads][dim], its heads and elements packed in a
+    row.  `device`: the CUDA device's index."""
+    if t.dtype is not dtype or t.get_device() != device:
+        raise Q4Error(Q4_EINVAL, f"{name}: {t.dtype} on {t.device}, {dtype} on cuda:{device} expected")
     if t.dim() != 3:
         raise Q4Error(Q4_ESHAPE, f"{name}: shape {tuple(t.shape)}, [rows][heads][dim] expected")
     n, m, d = t.shape
-    if (rows is not None and n != rows) or (heads is not None and m != heads) or (dim is not None and d != dim):
-        raise Q4Error(Q4_ESHAPE, f"{name}: shape {tuple(t.shape)}, ({rows}, {heads}, {dim}) expected")
     rs, hs, es = t.stride()
     if (es != 1 and d != 1) or (hs != d and m != 1):
         raise Q4Error(Q4_ESHAPE, f"{name}: the heads of a row must lie one after the other")
-    return rs if n > 1 else m * d          # torch gives a single row any stride
+    return n, m, d, rs if n > 1 else m * d          # torch gives a single row any stride
+
+
+def _want(name: str, got, want):
+    raise Q4Error(Q4_ESHAPE, f"{name}: shape {got}, {want} expected")
 
 
 def _ints(t, name: str, device, n: int):
-    if t.dtype is not _torch.int32 or t.device != device:
-        raise Q4Error(Q4_EINVAL, f"{name}: {t.dtype} on {t.device}, int32 on {device} expected")
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype is not _torch.int32 or t.get_device() != device:
+        raise Q4Error(Q4_EINVAL, f"{name}: {t.dtype} on {t.device}, int32 on cuda:{device} expected")
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise Q4Error(Q4_ESHAPE, f"{name}: {n} contiguous entries expected")
     return t.data_ptr()
 
@@ -362,6 +366,7 @@ class PagedKV:
         self.k, self.v, self.table = k, v, table
         self.device, self.dtype = k.device, k.dtype
         pages, size, heads, dim = k.shape
+        self.index, self.heads, self.dim, self.seqs = k.get_device(), heads, dim, table.shape[0]
         ps, ts, hs, _ = k.stride()
         cols = table.shape[1]
         self.args = q4gemv_kv(k.data_ptr(), v.data_ptr(), table.data_ptr(), pages, size, heads, dim, ps, ts, hs,
@@ -505,9 +510,9 @@ class Q4Gemv:
     # ---- token mixing: start int32 [sequences + 1] (rows of each sequence), length int32
     # [sequences] (its tokens in the cache, the new ones counted), all on the handle's device ----
 
-    def _on_device(self, device):
-        if device.type != "cuda" or device.index != self.device:
-            raise Q4Error(Q4_EINVAL, f"tensors on {device}, the handle is on cuda:{self.device}")
+    def _on_device(self, index):
+        if index != self.device:
+            raise Q4Error(Q4_EINVAL, f"tensors on device {index}, the handle is on cuda:{self.device}")
 
     def _stream_of(self, stream) -> int:
         if stream is None:
@@ -536,54 +541,62 @@ class Q4Gemv:
         """Appends k, v [rows][heads][head_dim] to the cache, k rotated; returns q
         [rows][q_heads][head_dim] rotated (None without q).  freqs: float64 [rot/2] or None (no
         rotation); pos: int32 [rows] rotation positions, by default the places in the cache."""
-        self._on_device(cache.device)
-        c = cache.args
-        n_seqs = length.shape[0]
-        if cache.table.shape[0] < n_seqs:
+        dev, dt, heads, dim = cache.index, cache.dtype, cache.heads, cache.dim
+        self._on_device(dev)
+        n_seqs = length.numel()
+        if cache.seqs < n_seqs:
             raise Q4Error(Q4_ESHAPE, "fewer page-table rows than sequences")
-        rows = k.shape[0]
-        ks = _heads(k, "k", cache.dtype, cache.device, None, c.n_heads, c.head_dim)
-        vs = _heads(v, "v", cache.dtype, cache.device, rows, c.n_heads, c.head_dim)
+        rows, m, d, ks = _rows(k, "k", dt, dev)
+        if m != heads or d != dim:
+            _want("k", (rows, m, d), (rows, heads, dim))
+        n, m, d, vs = _rows(v, "v", dt, dev)
+        if n != rows or m != heads or d != dim:
+            _want("v", (n, m, d), (rows, heads, dim))
         qs = qos = hq = 0
         qp = qop = None
         if q is not None:
-            hq = q.shape[1]
-            qs = _heads(q, "q", cache.dtype, cache.device, rows, None, c.head_dim)
+            n, hq, d, qs = _rows(q, "q", dt, dev)
+            if n != rows or d != dim:
+                _want("q", (n, hq, d), (rows, hq, dim))
             if q_out is None:
                 q_out = self._new(q.shape, q.dtype, stream)
-            qos = _heads(q_out, "q_out", cache.dtype, cache.device, rows, hq, c.head_dim)
+            n, m, d, qos = _rows(q_out, "q_out", dt, dev)
+            if n != rows or m != hq or d != dim:
+                _want("q_out", (n, m, d), (rows, hq, dim))
             qp, qop = q.data_ptr(), q_out.data_ptr()
         rope = None
         if freqs is not None:
-            if freqs.dtype != _torch.float64 or freqs.device != cache.device or not freqs.is_contiguous():
+            if freqs.dtype is not _torch.float64 or freqs.get_device() != dev or not freqs.is_contiguous():
                 raise Q4Error(Q4_EINVAL, "freqs: contiguous float64 on the cache's device expected")
-            rope = q4gemv_rope(freqs.data_ptr(), 2 * freqs.numel(), int(interleaved), amp)
-        self._check(_lib.q4gemv_kv_append(
-            self.h, cache.ref, rows, n_seqs, _ints(start, "start", cache.device, n_seqs + 1),
-            _ints(length, "length", cache.device, n_seqs),
-            None if pos is None else _ints(pos, "pos", cache.device, rows), rope, qp, qs, hq,
-            k.data_ptr(), ks, v.data_ptr(), vs, qop, qos, self._stream_of(stream)))
+            rope = q4gemv_rope(freqs.data_ptr(), 2 * freqs.numel(), interleaved, amp)
+        self._check(_kv_append(
+            self.h, cache.ref, rows, n_seqs, _ints(start, "start", dev, n_seqs + 1),
+            _ints(length, "length", dev, n_seqs), None if pos is None else _ints(pos, "pos", dev, rows), rope,
+            qp, qs, hq, k.data_ptr(), ks, v.data_ptr(), vs, qop, qos, self._stream_of(stream)))
         return q_out if q is not None else None
 
     def attn_paged(self, cache, start, length, q, out=None, scale: float | None = None,
                    causal: bool = True, window: int = 0, max_new: int | None = None, stream=None):
         """Attention of q [rows][q_heads][head_dim] over the cache (default scale
         1/sqrt(head_dim)); max_new: the most new tokens of a sequence, where known."""
-        self._on_device(cache.device)
-        c = cache.args
-        n_seqs = length.shape[0]
-        if cache.table.shape[0] < n_seqs:
+        dev, dt, dim = cache.index, cache.dtype, cache.dim
+        self._on_device(dev)
+        n_seqs = length.numel()
+        if cache.seqs < n_seqs:
             raise Q4Error(Q4_ESHAPE, "fewer page-table rows than sequences")
-        qs = _heads(q, "q", cache.dtype, cache.device, None, None, c.head_dim)
-        rows, hq = q.shape[0], q.shape[1]
+        rows, hq, d, qs = _rows(q, "q", dt, dev)
+        if d != dim:
+            _want("q", (rows, hq, d), (rows, hq, dim))
         if out is None:
             out = self._new(q.shape, q.dtype, stream)
-        os_ = _heads(out, "out", cache.dtype, cache.device, rows, hq, c.head_dim)
-        self._check(_lib.q4gemv_attn_paged(
-            self.h, cache.ref, rows, n_seqs, _ints(start, "start", cache.device, n_seqs + 1),
-            _ints(length, "length", cache.device, n_seqs), max(1, rows) if max_new is None else max_new,
-            q.data_ptr(), qs, hq, out.data_ptr(), os_,
-            c.head_dim ** -0.5 if scale is None else scale, int(causal), window, self._stream_of(stream)))
+        n, m, d, os_ = _rows(out, "out", dt, dev)
+        if n != rows or m != hq or d != dim:
+            _want("out", (n, m, d), (rows, hq, dim))
+        self._check(_attn_paged(
+            self.h, cache.ref, rows, n_seqs, _ints(start, "start", dev, n_seqs + 1),
+            _ints(length, "length", dev, n_seqs), (rows or 1) if max_new is None else max_new,
+            q.data_ptr(), qs, hq, out.data_ptr(), os_, dim ** -0.5 if scale is None else scale,
+            causal, window, self._stream_of(stream)))
         return out
 
     def linattn(self, q, k, v, log_decay, start, state, state_out=None, slots=None, scale: float = 1.0,
@@ -596,32 +609,39 @@ class Q4Gemv:
             state_out = state
         if state_out is None:
             raise Q4Error(Q4_EINVAL, "linattn: neither state nor state_out")
-        dev = state_out.device
+        dev = state_out.get_device()
         self._on_device(dev)
-        n_seqs = start.shape[0] - 1
-        dt = _dtype_code(q)
-        qs = _heads(q, "q", q.dtype, dev)
-        rows, hk, dk = q.shape
-        ks = _heads(k, "k", q.dtype, dev, rows, hk, dk)
-        hv, dv = v.shape[1], v.shape[2]
-        vs = _heads(v, "v", q.dtype, dev, rows)
+        n_seqs = start.numel() - 1
+        dt, code = q.dtype, _dtype_code(q)
+        rows, hk, dk, qs = _rows(q, "q", dt, dev)
+        n, m, d, ks = _rows(k, "k", dt, dev)
+        if n != rows or m != hk or d != dk:
+            _want("k", (n, m, d), (rows, hk, dk))
+        n, hv, dv, vs = _rows(v, "v", dt, dev)
+        if n != rows:
+            _want("v", (n, hv, dv), (rows, hv, dv))
         if out is None:
-            out = self._new((rows, hv, dv), q.dtype, stream)
-        os_ = _heads(out, "out", q.dtype, dev, rows, hv, dv)
-        if log_decay.dtype != _torch.float32 or log_decay.device != dev or log_decay.shape != (rows, hv) or \
-                (hv > 1 and log_decay.stride(1) != 1):
-            raise Q4Error(Q4_ESHAPE, f"log_decay: float32 [{rows}][{hv}] on {dev} expected")
-        n_slots = state_out.shape[0]
-        for t in (state, state_out):
-            if t is not None and (t.dtype != _torch.float32 or t.device != dev or not t.is_contiguous() or
-                                  t.shape != (n_slots, hv, dk, dv)):
-                raise Q4Error(Q4_ESHAPE, f"state: contiguous float32 [{n_slots}][{hv}][{dk}][{dv}] on {dev} expected")
+            out = self._new((rows, hv, dv), dt, stream)
+        n, m, d, os_ = _rows(out, "out", dt, dev)
+        if n != rows or m != hv or d != dv:
+            _want("out", (n, m, d), (rows, hv, dv))
+        if log_decay.dtype is not _torch.float32 or log_decay.get_device() != dev or \
+                log_decay.shape != (rows, hv) or (hv > 1 and log_decay.stride(1) != 1):
+            raise Q4Error(Q4_ESHAPE, f"log_decay: float32 [{rows}][{hv}] on cuda:{dev} expected")
+        shape = state_out.shape
+        if len(shape) != 4 or shape[1:] != (hv, dk, dv) or state_out.dtype is not _torch.float32 or \
+                not state_out.is_contiguous() or \
+                (state is not None and state is not state_out and
+                 (state.shape != shape or state.dtype is not _torch.float32 or state.get_device() != dev or
+                  not state.is_contiguous())):
+            raise Q4Error(Q4_ESHAPE, f"state: contiguous float32 [slots][{hv}][{dk}][{dv}] on cuda:{dev} expected, "
+                          "the same for state_out")
         a = q4gemv_linattn_args(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state), state_out.data_ptr(),
             None if slots is None else _ints(slots, "slots", dev, n_seqs), out.data_ptr(), qs, ks, vs,
-            log_decay.stride(0) if rows > 1 else hv, os_, n_slots, hk, hv, dk, dv, scale, dt)
-        self._check(_lib.q4gemv_linattn(self.h, a, rows, n_seqs, _ints(start, "start", dev, n_seqs + 1),
-                                        max(1, rows) if max_new is None else max_new, self._stream_of(stream)))
+            log_decay.stride(0) if rows > 1 else hv, os_, shape[0], hk, hv, dk, dv, scale, code)
+        self._check(_linattn(self.h, a, rows, n_seqs, _ints(start, "start", dev, n_seqs + 1),
+                             (rows or 1) if max_new is None else max_new, self._stream_of(stream)))
         return out, state_out
 
     def sync_status(self, stream=None) -> int:
