@@ -582,6 +582,44 @@ Q4GEMV_API int q4gemv_linattn(q4gemv_t h, const q4gemv_linattn_args* args, int64
                               int64_t n_seqs, const int32_t* start, int64_t max_new,
                               q4gemv_stream_t stream);
 
+/* A layer's token mixer in q4gemv_run_stack_mixed: attention over a paged cache
+ * (table row 0 is the sequence's), or linear attention with fixed decays. */
+enum { Q4GEMV_MIX_ATTENTION = 0, Q4GEMV_MIX_LINEAR = 1 };
+typedef struct {
+    int kind;
+    q4gemv_kv kv;            /* attention: binary16, n_heads = kv_heads, head_dim = hidden/q_heads */
+    const float* log_decay;  /* linear: device, [q_heads] */
+    float* state;            /* linear: device, [q_heads][head_dim][head_dim], updated */
+} q4gemv_mixer;
+
+/* The decode step of q4gemv_run_stack_gated for one token of one sequence with
+ * a token mixer between the QKV and the O product of every layer, in place of
+ * the Q slice: the hybrid trunk's step.  With D = hidden / q_heads the QKV
+ * product has hidden + 2 kv_heads D outputs a, and
+ *   attention: a = [q | k | v] (q_heads, kv_heads, kv_heads heads of D); k
+ *              (rotated) and v are appended to the layer's cache at place
+ *              len[0] - 1 and the rotated q attends to the len[0] tokens there,
+ *              scores times 1/sqrt(D): q4gemv_kv_append, q4gemv_attn_paged;
+ *   linear:    a = [q | k | v] (kv_heads, kv_heads, q_heads heads of D):
+ *              q4gemv_linattn with scale 1/sqrt(D) on the layer's state;
+ * the mixer's output m (hidden binary16) goes to O, scaled to unit RMS like
+ * every input of the chain: b = f16(s(m) O m).  Everything else as
+ * q4gemv_run_stack_gated.
+ *   layers, mixers : HOST arrays of n_layers entries (device pointers inside)
+ *   rope    : host struct or NULL (device pointer inside), as q4gemv_kv_append
+ *   len     : device, one entry: the sequence's tokens, the new one counted; the
+ *             caller advances it between steps
+ *   x_in, x_out : device, hidden binary16 (x_out may alias x_in)
+ * Launches its kernels on `stream` (4 products and 1 or 2 mixer kernels a
+ * layer), so it may be captured into a graph and replayed token by token; the
+ * first call with larger sizes must come outside a capture.  Errors of the
+ * parts it runs; Q4_ESHAPE if q_heads does not divide hidden, kv_heads does not
+ * divide q_heads, or a layer's cache has other heads. */
+Q4GEMV_API int q4gemv_run_stack_mixed(q4gemv_t h, const q4gemv_layer* layers, const q4gemv_mixer* mixers,
+                                      int n_layers, int64_t hidden, int64_t ffn, int64_t q_heads,
+                                      int64_t kv_heads, const q4gemv_rope* rope, const int32_t* len,
+                                      const void* x_in, void* x_out, q4gemv_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the handle's device error
  * word: Q4_OK, Q4_ETIMEOUT, Q4_ECONCURRENT, Q4_EINDEX, or Q4_ECUDA if an earlier
  * asynchronous error is pending on the device. */

@@ -30,6 +30,7 @@ MAX_M = 256        # vectors per q4gemv_run call
 MAX_M_GEMV = 16    # above this, the tensor-core GEMM path
 F16, BF16 = 0, 1   # q4gemv_dtype
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BY_PARTS = 0, 1, 2
+MIX_ATTENTION, MIX_LINEAR = 0, 1
 
 
 class Q4Error(RuntimeError):
@@ -67,6 +68,11 @@ class q4gemv_linattn_args(ctypes.Structure):
                 ("qk_heads", ctypes.c_int64), ("v_heads", ctypes.c_int64),
                 ("k_dim", ctypes.c_int64), ("v_dim", ctypes.c_int64),
                 ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+class q4gemv_mixer(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("kv", q4gemv_kv), ("log_decay", ctypes.c_void_p),
+                ("state", ctypes.c_void_p)]
 
 
 def _load_library():
@@ -117,6 +123,8 @@ def _load_library():
                               vp], ci),
         "q4gemv_attn_paged": ([vp, ctypes.POINTER(q4gemv_kv), i64, i64, vp, vp, i64, vp, i64, i64, vp,
                                i64, ctypes.c_float, ci, i64, vp], ci),
+        "q4gemv_run_stack_mixed": ([vp, ctypes.POINTER(q4gemv_layer), ctypes.POINTER(q4gemv_mixer), ci, i64,
+                                    i64, i64, i64, ctypes.POINTER(q4gemv_rope), vp, vp, vp, vp], ci),
         "q4gemv_linattn": ([vp, ctypes.POINTER(q4gemv_linattn_args), i64, i64, vp, i64, vp], ci),
     }
     for name, (args, res) in sigs.items():
@@ -293,6 +301,12 @@ def q4gemv_attn_paged(h, kv, rows, n_seqs, start, length, max_new, q, q_stride, 
 
 def q4gemv_linattn(h, args, rows, n_seqs, start, max_new, stream) -> int:
     return _lib.q4gemv_linattn(h, args, rows, n_seqs, start, max_new, stream)
+
+
+def q4gemv_run_stack_mixed(h, layers, mixers, n_layers, hidden, ffn, q_heads, kv_heads, rope, length, x_in,
+                           x_out, stream) -> int:
+    return _lib.q4gemv_run_stack_mixed(h, layers, mixers, n_layers, hidden, ffn, q_heads, kv_heads, rope,
+                                       length, x_in, x_out, stream)
 
 
 def _ptr(t) -> int | None:
@@ -643,6 +657,45 @@ class Q4Gemv:
         self._check(_linattn(self.h, a, rows, n_seqs, _ints(start, "start", dev, n_seqs + 1),
                              (rows or 1) if max_new is None else max_new, self._stream_of(stream)))
         return out, state_out
+
+    def run_stack_mixed(self, layers, mixers, x_in, hidden: int, ffn: int, q_heads: int, kv_heads: int,
+                        length, freqs=None, interleaved: bool = False, amp: float = 1.0, x_out=None,
+                        stream=None):
+        """One token's decode step with a token mixer in every layer.  layers: (qkv, o, gate_up,
+        down) packed tensors; mixers: for each layer a PagedKV (attention) or a pair (log_decay
+        float32 [q_heads], state float32 [q_heads][D][D]) (linear attention), D = hidden/q_heads;
+        length: int32 [1], the sequence's tokens with this one."""
+        d = hidden // q_heads
+        if len(mixers) != len(layers):
+            raise Q4Error(Q4_ESHAPE, "run_stack_mixed: one mixer a layer expected")
+        if x_in.dtype is not _torch.float16 or x_in.numel() != hidden or not x_in.is_contiguous():
+            raise Q4Error(Q4_ESHAPE, f"x_in: contiguous float16 [{hidden}] expected")
+        self._on_device(x_in.get_device())
+        la = (q4gemv_layer * len(layers))(*[q4gemv_layer(*(t.data_ptr() for t in row)) for row in layers])
+        ma = (q4gemv_mixer * len(layers))()
+        for i, m in enumerate(mixers):
+            if isinstance(m, PagedKV):
+                self._on_device(m.index)
+                ma[i] = q4gemv_mixer(MIX_ATTENTION, m.args, None, None)
+                continue
+            g, s = m
+            for t, shape in ((g, (q_heads,)), (s, (q_heads, d, d))):
+                if t.dtype is not _torch.float32 or t.shape != shape or not t.is_contiguous():
+                    raise Q4Error(Q4_ESHAPE, f"mixer {i}: contiguous float32 {shape} expected")
+                self._on_device(t.get_device())
+            ma[i] = q4gemv_mixer(MIX_LINEAR, q4gemv_kv(), g.data_ptr(), s.data_ptr())
+        rope = None
+        if freqs is not None:
+            if freqs.dtype is not _torch.float64 or not freqs.is_contiguous():
+                raise Q4Error(Q4_EINVAL, "freqs: contiguous float64 expected")
+            self._on_device(freqs.get_device())
+            rope = q4gemv_rope(freqs.data_ptr(), 2 * freqs.numel(), interleaved, amp)
+        if x_out is None:
+            x_out = self._new((hidden,), _torch.float16, stream)
+        self._check(_lib.q4gemv_run_stack_mixed(
+            self.h, la, ma, len(layers), hidden, ffn, q_heads, kv_heads, rope,
+            _ints(length, "length", self.device, 1), x_in.data_ptr(), x_out.data_ptr(), self._stream_of(stream)))
+        return x_out
 
     def sync_status(self, stream=None) -> int:
         return q4gemv_sync_status(self.h, _stream(stream))

@@ -6,6 +6,7 @@
 #include <nccl.h>   // types only: the functions are resolved at run time
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -36,6 +37,7 @@ constexpr int kMinSegsPerWarp = 4;         // small problems use fewer warps
 constexpr int kMaxTiles = Q4GEMV_MAX_N / 32;
 constexpr size_t kMaxDynSmem = 224 * 1024;   // opt-in dynamic shared memory per CTA
 constexpr size_t kYaccPrealloc = (size_t)1 << 21;   // fp32 panel accumulator floats at create
+constexpr int kOneRow[2] = {0, 1};         // start of a batch of one token
 constexpr size_t kXimgPrealloc = (size_t)1 << 24;   // GEMM activation image bytes at create
 static_assert(q4::kTcMaxVec == Q4GEMV_MAX_M, "the GEMM's MMA width bounds M");
 
@@ -129,6 +131,9 @@ struct q4gemv_ctx {
     float* attn_ws = nullptr;        // shared pieces of the paged attention, and their counts
     int* attn_cnt = nullptr;
     size_t attn_ws_bytes = 0;
+    __half* mix_act = nullptr;       // vectors of the step with mixers
+    size_t mix_act_elems = 0;
+    int* mix_start = nullptr;        // {0, 1}: its one row
     uint8_t* ximg = nullptr;         // activation image of the tensor-core GEMM
     size_t ximg_bytes = 0;
     int64_t hio_elems = 0;           // per vector
@@ -793,7 +798,8 @@ int q4gemv_create(q4gemv_t* out, int device) {
             cudaMalloc(&h->yacc, kYaccPrealloc * sizeof(float)) != cudaSuccess ||
             cudaMalloc(&h->ximg, kXimgPrealloc) != cudaSuccess ||
             cudaMalloc(&h->attn_ws, attn_ws_bytes) != cudaSuccess ||
-            cudaMalloc(&h->attn_cnt, attn_cnt_bytes) != cudaSuccess)
+            cudaMalloc(&h->attn_cnt, attn_cnt_bytes) != cudaSuccess ||
+            cudaMalloc(&h->mix_start, 2 * sizeof(int)) != cudaSuccess)
             rc = fail(h, Q4_ENOMEM, "workspace allocation failed");
         else {
             h->yacc_floats = kYaccPrealloc;
@@ -809,7 +815,8 @@ int q4gemv_create(q4gemv_t* out, int device) {
     if (rc == Q4_OK) {
         if (cudaMemset(h->cnt, 0, (size_t)kMaxTiles * sizeof(int)) != cudaSuccess ||
             cudaMemset(h->err, 0, sizeof(int)) != cudaSuccess ||
-            cudaMemset(h->attn_cnt, 0, attn_cnt_bytes) != cudaSuccess)
+            cudaMemset(h->attn_cnt, 0, attn_cnt_bytes) != cudaSuccess ||
+            cudaMemcpy(h->mix_start, kOneRow, sizeof kOneRow, cudaMemcpyHostToDevice) != cudaSuccess)
             rc = fail(h, Q4_ECUDA, "workspace initialisation failed");
     }
     if (rc == Q4_OK) {
@@ -845,6 +852,7 @@ int q4gemv_create(q4gemv_t* out, int device) {
         cudaFree(h->ximg);
         cudaFree(h->attn_ws);
         cudaFree(h->attn_cnt);
+        cudaFree(h->mix_start);
         if (h->cap) cudaStreamDestroy(h->cap);
         delete h;
         return rc;
@@ -871,6 +879,8 @@ int q4gemv_destroy(q4gemv_t h) {
     cudaFree(h->ximg);
     cudaFree(h->attn_ws);
     cudaFree(h->attn_cnt);
+    cudaFree(h->mix_start);
+    cudaFree(h->mix_act);
     cudaFree(h->gscr);
     shard_release(h);
     peer_release(h);
@@ -1279,6 +1289,106 @@ int q4gemv_run_stack_gated(q4gemv_t h, const q4gemv_layer* layers, int n_layers,
                            q4gemv_stream_t stream) {
     return run_stack_impl(h, layers, n_layers, hidden, qkv_n, ffn, x_in, x_out, nullptr, nullptr, stream,
                           true);
+}
+
+int q4gemv_run_stack_mixed(q4gemv_t h, const q4gemv_layer* layers, const q4gemv_mixer* mixers, int n_layers,
+                           int64_t hidden, int64_t ffn, int64_t q_heads, int64_t kv_heads, const q4gemv_rope* rope,
+                           const int32_t* len, const void* x_in, void* x_out, q4gemv_stream_t stream) {
+    if (!h) return Q4_EINVAL;
+    if (!layers || !mixers || !len || !x_in || !x_out) return fail(h, Q4_EINVAL, "run_stack_mixed: null pointer");
+    if (n_layers < 1 || n_layers > 4096) return fail(h, Q4_ESHAPE, "run_stack_mixed: n_layers out of range");
+    if (q_heads < 1 || kv_heads < 1 || hidden < 1 || hidden % q_heads != 0 || q_heads % kv_heads != 0)
+        return fail(h, Q4_ESHAPE, "run_stack_mixed: heads do not divide");
+    const int64_t D = hidden / q_heads, kvn = kv_heads * D, qkv_n = hidden + 2 * kvn;
+    if (D % 8 != 0 || D > Q4GEMV_MAX_HEAD_DIM)
+        return fail(h, Q4_ESHAPE, "run_stack_mixed: head size is not a multiple of 8 up to 256");
+    const int64_t n_of[4] = {qkv_n, hidden, 2 * ffn, hidden}, k_of[4] = {hidden, hidden, hidden, ffn};
+    for (int t = 0; t < 4; ++t) {
+        const int s = check_shape(n_of[t], k_of[t]);
+        if (s != Q4_OK) return fail(h, s, "run_stack_mixed: invalid matrix shape");
+        if (!dp2a_fits(1, k_of[t])) return fail(h, Q4_EUNSUPPORTED, "run_stack_mixed: K too large");
+    }
+    if (is_host_pointer(x_in) || is_host_pointer(x_out))
+        return fail(h, Q4_EINVAL, "run_stack_mixed: x_in and x_out must be device memory");
+    if (!aligned16(x_in) || !aligned16(x_out)) return fail(h, Q4_EALIGN, "run_stack_mixed: misaligned vector");
+    for (int l = 0; l < n_layers; ++l) {
+        const q4gemv_layer& L = layers[l];
+        const q4gemv_mixer& m = mixers[l];
+        if (!L.qkv || !L.o || !L.gate_up || !L.down)
+            return fail(h, Q4_EINVAL, "run_stack_mixed: null matrix in layer %d", l);
+        if (!aligned16(L.qkv) || !aligned16(L.o) || !aligned16(L.gate_up) || !aligned16(L.down))
+            return fail(h, Q4_EALIGN, "run_stack_mixed: misaligned matrix in layer %d", l);
+        if (m.kind == Q4GEMV_MIX_ATTENTION) {
+            if (m.kv.dtype != Q4GEMV_F16 || m.kv.n_heads != kv_heads || m.kv.head_dim != D)
+                return fail(h, Q4_ESHAPE, "run_stack_mixed: the cache of layer %d has other heads", l);
+        } else if (m.kind == Q4GEMV_MIX_LINEAR) {
+            if (!m.log_decay || !m.state) return fail(h, Q4_EINVAL, "run_stack_mixed: null state in layer %d", l);
+        } else {
+            return fail(h, Q4_EINVAL, "run_stack_mixed: unknown mixer in layer %d", l);
+        }
+    }
+    Q4_CUDA(h, cudaSetDevice(h->device));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // QKV, rotated queries, mixer, O, gate+up and down outputs.
+    const int64_t parts[6] = {qkv_n, hidden, hidden, hidden, 2 * ffn, hidden};
+    int64_t off[7] = {0};
+    for (int i = 0; i < 6; ++i) off[i + 1] = off[i] + (parts[i] + 7) / 8 * 8;
+    if ((size_t)off[6] > h->mix_act_elems) {
+        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+        Q4_CUDA(h, cudaStreamIsCapturing(st, &cs));
+        if (cs != cudaStreamCaptureStatusNone)
+            return fail(h, Q4_EUNSUPPORTED, "run_stack_mixed: first call with these sizes must happen outside stream capture");
+        if (h->fault == kFaultAlloc) return fail(h, Q4_EFAULTINJ, "injected allocation failure");
+        Q4_CUDA(h, cudaDeviceSynchronize());
+        cudaFree(h->mix_act);
+        h->mix_act = nullptr;
+        h->mix_act_elems = 0;
+        if (cudaMalloc(&h->mix_act, (size_t)off[6] * sizeof(__half)) != cudaSuccess)
+            return fail(h, Q4_ENOMEM, "run_stack_mixed: activation buffer allocation failed");
+        h->mix_act_elems = (size_t)off[6];
+    }
+    __half* buf[6];
+    for (int i = 0; i < 6; ++i) buf[i] = h->mix_act + off[i];
+    const float scale = 1.f / sqrtf((float)D);
+    const __half* x = static_cast<const __half*>(x_in);
+    for (int l = 0; l < n_layers; ++l) {
+        const q4gemv_layer& L = layers[l];
+        const q4gemv_mixer& m = mixers[l];
+        int rc = launch_gemv(h, L.qkv, x, buf[0], 1, qkv_n, hidden, l > 0 ? 1 : 0, nullptr, st, l > 0);
+        if (rc != Q4_OK) return rc;
+        if (m.kind == Q4GEMV_MIX_ATTENTION) {
+            const __half *k = buf[0] + hidden, *v = k + kvn;
+            rc = q4gemv_kv_append(h, &m.kv, 1, 1, h->mix_start, len, nullptr, rope, buf[0], hidden, q_heads, k, kvn, v,
+                                  kvn, buf[1], hidden, stream);
+            if (rc == Q4_OK)
+                rc = q4gemv_attn_paged(h, &m.kv, 1, 1, h->mix_start, len, 1, buf[1], hidden, q_heads, buf[2], hidden, scale,
+                                       1, 0, stream);
+        } else {
+            q4gemv_linattn_args a = {};
+            a.q = buf[0];
+            a.k = buf[0] + kvn;
+            a.v = buf[0] + 2 * kvn;
+            a.log_decay = m.log_decay;
+            a.state_in = a.state_out = m.state;
+            a.out = buf[2];
+            a.q_stride = a.k_stride = kvn;
+            a.v_stride = a.out_stride = hidden;
+            a.n_slots = 1;
+            a.qk_heads = kv_heads;
+            a.v_heads = q_heads;
+            a.k_dim = a.v_dim = D;
+            a.scale = scale;
+            a.dtype = Q4GEMV_F16;
+            rc = q4gemv_linattn(h, &a, 1, 1, h->mix_start, 1, stream);
+        }
+        if (rc != Q4_OK) return rc;
+        if ((rc = launch_gemv(h, L.o, buf[2], buf[3], 1, hidden, hidden, 1, nullptr, st, true)) != Q4_OK) return rc;
+        if ((rc = launch_gemv(h, L.gate_up, buf[3], buf[4], 1, 2 * ffn, hidden, 1, nullptr, st, true)) != Q4_OK) return rc;
+        if ((rc = launch_gemv(h, L.down, buf[4], buf[5], 1, hidden, ffn, 1, nullptr, st, true, false, true)) != Q4_OK)
+            return rc;
+        x = buf[5];
+    }
+    return launch_renorm(h, x, static_cast<__half*>(x_out), (int)hidden, st, true);
 }
 
 int q4gemv_shard_rows(int64_t N, int world, int rank, int64_t* row0, int64_t* rows, int64_t* chunk) {
