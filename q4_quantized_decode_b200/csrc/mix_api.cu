@@ -126,10 +126,17 @@ q4::RaggedArgs ragged(int64_t rows, int64_t n_seqs, const int32_t* start, const 
     return b;
 }
 
-// Rows of a sequence up to which attn_split_kernel takes it.
-constexpr int kSplitRowsMax = 128;
-// Up to this many new tokens of a sequence run token by token.
-constexpr int kLinRecurMax = 8;
+// Up to this many rows of a sequence always go to attn_split_kernel, and up to
+// as many as keep all its tiles' reads (tiles of 16 rows x key heads x cached
+// tokens, by the table's capacity) under kSplitReads.  Measured (us, that
+// kernel / the tensor-core one): 320 rows of 8 key heads of 128 over 1000 tokens
+// 32 / 36, 640 rows 48 / 36; 80 rows over 30000 tokens 111 / 90; 1024 rows of
+// one key head of 64 over 8000 tokens 39 / 43.
+constexpr int kSplitRowsMin = 64, kSplitRowsMax = 1024;
+constexpr int64_t kSplitReads = 300000;
+// Up to this many new tokens of a sequence run token by token (us a token and
+// head-parallel step: 0.65; a chunk of up to 128 tokens costs 11).
+constexpr int kLinRecurMax = 12;
 // Chunks of a prompt's segment, at least.
 constexpr int kLinSegChunks = 4;
 
@@ -380,14 +387,16 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
     // Sequences with many rows (new tokens times query heads of a key head) go
     // to the tensor-core kernel, those with few to the other; a batch that may
     // hold both runs both.
-    const bool many = kv->head_dim <= 128 && max_new > kSplitRowsMax / a.group;
+    const int64_t reads = kv->n_heads * n_seqs * (int64_t)a.cap;     // of one tile of each sequence
+    const int limit = (int)std::max<int64_t>(kSplitRowsMin, std::min<int64_t>(kSplitRowsMax, 16 * (kSplitReads / reads)));
+    const bool many = kv->head_dim <= 128 && max_new > limit / a.group;
     const bool few = !many || n_seqs > 1;
     if (many) {
         q4::TcAttnArgs g;
         g.a = a;
         g.ws = cx.attn_ws;
         g.cnt = cx.attn_cnt;
-        g.min_rows = few ? kSplitRowsMax : 0;
+        g.min_rows = few ? limit : 0;
         const int dp = kv->head_dim <= 64 ? 64 : 128;
         // Boxes of the largest power of two of tokens that divides a page, up
         // to a tile; under 8 they would be more than the 16-byte copies' work.
@@ -403,7 +412,7 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
     g.a = a;
     g.ws = cx.attn_ws;
     g.cnt = cx.attn_cnt;
-    g.max_rows = many ? kSplitRowsMax : 0;
+    g.max_rows = many ? limit : 0;
     return launch_status(h, f16 ? split_launch<__half>(g, cx.sms, st) : split_launch<__nv_bfloat16>(g, cx.sms, st), call);
 }
 

@@ -203,12 +203,18 @@ def test_append_bad_pages_are_reported(eng):
 
 # ---- attend -----------------------------------------------------------------
 
+# Columns of the page table: a table that could hold long contexts sends
+# sequences of more than 64 rows to the tensor-core kernel.
+WIDE = 1 << 14
+
+
 class AttendCase:
-    def __init__(self, new, length, hq, hkv, dim, page, dtype, seed=0, head_major=False, poison=True, amp=1.0):
+    def __init__(self, new, length, hq, hkv, dim, page, dtype, seed=0, head_major=False, poison=True, amp=1.0,
+                 cols=0):
         gen = torch.Generator().manual_seed(seed)
         self.new, self.length, self.hq, self.hkv, self.dim, self.dtype = new, length, hq, hkv, dim, dtype
         self.rows = sum(new)
-        self.table, pool = ref.table_of(length, page, gen)
+        self.table, pool = ref.table_of(length, page, gen, cols=cols)
         self.k, self.v = (ref.paged(pool, page, hkv, dim, dtype, gen, head_major) for _ in range(2))
         if poison:                                       # what no token has written is NaN
             used = torch.zeros(pool, page, dtype=torch.bool)
@@ -252,64 +258,70 @@ def test_attend_single_tokens(eng, dtype, hq, hkv, dim):
     c.check(out)
 
 
+@pytest.mark.parametrize("cols", [0, WIDE])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("page,head_major", [(1, False), (5, False), (16, True), (24, False), (100, True), (1024, False)])
-def test_attend_pages(eng, dtype, page, head_major):
-    c = AttendCase([1, 3, 70], [300, 77, 211], 4, 2, 64, page, dtype, seed=page, head_major=head_major)
+def test_attend_pages(eng, cols, dtype, page, head_major):
+    c = AttendCase([1, 3, 70], [300, 77, 211], 4, 2, 64, page, dtype, seed=page, head_major=head_major, cols=cols)
     out = c.run(eng, max_new=70)
     assert eng.sync_status() == q4.Q4_OK
     c.check(out)
 
 
+@pytest.mark.parametrize("cols", [0, WIDE])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("new,length", [([169], [169]), ([128, 0, 1, 33], [128, 40, 513, 1000]), ([200], [1300]),
                                         ([257, 64], [257, 65]), ([600], [600])])
 @pytest.mark.parametrize("hq,hkv,dim", [(5, 1, 128), (4, 4, 64), (2, 1, 256), (3, 1, 72)])
-def test_attend_chunks(eng, dtype, new, length, hq, hkv, dim):
-    c = AttendCase(new, length, hq, hkv, dim, 16, dtype, seed=sum(new) + dim)
+def test_attend_chunks(eng, cols, dtype, new, length, hq, hkv, dim):
+    c = AttendCase(new, length, hq, hkv, dim, 16, dtype, seed=sum(new) + dim, cols=cols)
     out = c.run(eng, max_new=max(new))
     assert eng.sync_status() == q4.Q4_OK
     c.check(out)
 
 
+@pytest.mark.parametrize("cols", [0, WIDE])
 @pytest.mark.parametrize("causal,window", [(True, 1), (True, 7), (True, 130), (True, 100000), (False, 0), (False, 40)])
 @pytest.mark.parametrize("new,length", [([1, 1], [500, 3]), ([4, 5], [260, 9]), ([150], [400])])
 @pytest.mark.parametrize("dim", [64, 128])
-def test_attend_masks(eng, causal, window, new, length, dim):
-    c = AttendCase(new, length, 4, 2, dim, 24, torch.float16, seed=window + sum(new))
+def test_attend_masks(eng, cols, causal, window, new, length, dim):
+    c = AttendCase(new, length, 4, 2, dim, 24, torch.float16, seed=window + sum(new), cols=cols)
     out = c.run(eng, causal=causal, window=window, max_new=max(new))
     assert eng.sync_status() == q4.Q4_OK
     c.check(out, causal=causal, window=window)
 
 
+@pytest.mark.parametrize("cols", [0, WIDE])
 @pytest.mark.parametrize("max_new", [1, 5, 1000])
-def test_attend_max_new_is_only_a_hint(eng, max_new):
-    c = AttendCase([1, 150, 0, 9], [900, 170, 8, 300], 6, 2, 128, 16, torch.float16, seed=9)
+def test_attend_max_new_is_only_a_hint(eng, cols, max_new):
+    c = AttendCase([1, 150, 0, 9], [900, 170, 8, 300], 6, 2, 128, 16, torch.float16, seed=9, cols=cols)
     out = c.run(eng, max_new=max_new)
     assert eng.sync_status() == q4.Q4_OK
     c.check(out)
 
 
+@pytest.mark.parametrize("cols", [0, WIDE])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("new", [3, 200])
-def test_attend_rows_that_see_nothing(eng, dim, new):
+def test_attend_rows_that_see_nothing(eng, cols, dim, new):
     """A length under the count of the new tokens: the first rows stand before
     the cache's beginning and see nothing; length 0: no row sees anything."""
-    c = AttendCase([new, new], [new - 2, 0], 2, 1, dim, 16, torch.float16, seed=dim)
+    c = AttendCase([new, new], [new - 2, 0], 2, 1, dim, 16, torch.float16, seed=dim, cols=cols)
     out = c.run(eng, max_new=new)
     assert eng.sync_status() == q4.Q4_OK
     assert (out[:2] == 0).all() and (out[new:] == 0).all()
     c.check(out)
 
 
+@pytest.mark.parametrize("cols", [0, WIDE])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("new", [4, 180])
-def test_attend_non_finite_values_of_unseen_tokens(eng, bad, dim, new):
+def test_attend_non_finite_values_of_unseen_tokens(eng, cols, bad, dim, new):
     """A later token of the chunk, or one before the window, holds NaN or Inf in
     its key and value: rows that do not see it are unaffected; rows that see it
     are not finite."""
-    c = AttendCase([new], [new + 50], 2, 1, dim, 16, torch.float16, seed=dim + new)
+    c = AttendCase([new], [new + 50], 2, 1, dim, 16, torch.float16, seed=dim + new, cols=cols)
     j = new + 50 - 2                                     # the last but one token
     pg, at = int(c.table[0, j // 16]), j % 16
     for pool in (c.k, c.v, c.cache.k, c.cache.v):
@@ -319,14 +331,14 @@ def test_attend_non_finite_values_of_unseen_tokens(eng, bad, dim, new):
     assert torch.isfinite(out[:new - 2]).all()
     if bad != bad:
         assert torch.isnan(out[new - 2:]).all()
-    clean = AttendCase([new], [new + 50], 2, 1, dim, 16, torch.float16, seed=dim + new)
+    clean = AttendCase([new], [new + 50], 2, 1, dim, 16, torch.float16, seed=dim + new, cols=cols)
     same = clean.run(eng, max_new=new)
     clean.check(same)
     same[:new - 2] = out[:new - 2]
     clean.check(same)
     # before the window
     w = 40
-    c2 = AttendCase([new], [new + 50], 2, 1, dim, 16, torch.float16, seed=dim + new)
+    c2 = AttendCase([new], [new + 50], 2, 1, dim, 16, torch.float16, seed=dim + new, cols=cols)
     pg, at = int(c2.table[0, 0]), 2
     for pool in (c2.k, c2.v, c2.cache.k, c2.cache.v):
         pool[pg, at, 0, :] = bad
@@ -335,11 +347,12 @@ def test_attend_non_finite_values_of_unseen_tokens(eng, bad, dim, new):
     c2.check(out, window=w)
 
 
-def test_attend_large_scores(eng):
+@pytest.mark.parametrize("cols", [0, WIDE])
+def test_attend_large_scores(eng, cols):
     """Scores of hundreds: one token takes all the weight; the running maximum
     has to follow."""
     for dim, new in ((64, 1), (128, 2), (128, 140), (64, 140), (256, 3)):
-        c = AttendCase([new], [600], 4, 2, dim, 16, torch.float16, seed=dim, amp=30.0)
+        c = AttendCase([new], [600], 4, 2, dim, 16, torch.float16, seed=dim, amp=30.0, cols=cols)
         out = c.run(eng, max_new=new)
         c.check(out)
         out = c.run(eng, max_new=new, scale=0.0)
@@ -349,9 +362,10 @@ def test_attend_large_scores(eng):
     assert eng.sync_status() == q4.Q4_OK
 
 
-def test_attend_strides_and_rows_of_no_sequence(eng):
+@pytest.mark.parametrize("cols", [0, WIDE])
+def test_attend_strides_and_rows_of_no_sequence(eng, cols):
     for new in ([1, 2], [90, 40]):
-        c = AttendCase(new, [70 + new[0], 200], 4, 2, 64, 16, torch.bfloat16, seed=11)
+        c = AttendCase(new, [70 + new[0], 200], 4, 2, 64, 16, torch.bfloat16, seed=11, cols=cols)
         rows = c.rows
         wide = torch.full((rows + 3, 4 * 64 + 24), 5.0, dtype=c.dtype, device=DEV)
         q = wide.clone()[:, :256].unflatten(1, (4, 64))
@@ -372,9 +386,10 @@ def test_attend_shared_pages(eng):
     assert eng.sync_status() == q4.Q4_OK
 
 
+@pytest.mark.parametrize("cols", [0, WIDE])
 @pytest.mark.parametrize("new", [1, 100])
-def test_attend_bad_pages_are_left_out(eng, new):
-    c = AttendCase([new, new], [200, 300], 4, 2, 128, 16, torch.float16, seed=13)
+def test_attend_bad_pages_are_left_out(eng, cols, new):
+    c = AttendCase([new, new], [200, 300], 4, 2, 128, 16, torch.float16, seed=13, cols=cols)
     good = c.cache.table.clone()
     c.cache.table[0, 3] = 10 ** 6
     c.cache.table[0, 4] = -1
@@ -397,10 +412,11 @@ def test_attend_bad_pages_are_left_out(eng, new):
     assert eng.sync_status() == q4.Q4_EINDEX
 
 
-def test_attend_is_deterministic_and_follows_a_graph(eng):
+@pytest.mark.parametrize("cols", [0, WIDE])
+def test_attend_is_deterministic_and_follows_a_graph(eng, cols):
     """A captured call replayed after the lengths, tables and queries changed."""
     for new in (1, 120):
-        c = AttendCase([new, new, new], [900, 130, 350], 8, 2, 128, 16, torch.float16, seed=14)
+        c = AttendCase([new, new, new], [900, 130, 350], 8, 2, 128, 16, torch.float16, seed=14, cols=cols)
         a, b = c.run(eng, max_new=new), c.run(eng, max_new=new)
         assert torch.equal(a, b)
         out = torch.zeros_like(c.gq)
@@ -412,7 +428,7 @@ def test_attend_is_deterministic_and_follows_a_graph(eng):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, a)
-        d = AttendCase([new, new, new], [500, 700, 121], 8, 2, 128, 16, torch.float16, seed=15)
+        d = AttendCase([new, new, new], [500, 700, 121], 8, 2, 128, 16, torch.float16, seed=15, cols=cols)
         n, cols = d.cache.k.shape[0], d.table.shape[1]
         assert n <= c.cache.k.shape[0] and cols <= c.table.shape[1]
         c.glen.copy_(d.glen)
@@ -435,7 +451,8 @@ def test_attend_long_context_offsets(eng):
     v = torch.zeros_like(k)
     gen = torch.Generator().manual_seed(1)
     for new in (1, 80):
-        table = torch.arange(pool - 7, pool, dtype=torch.int32)[None].flip(1).contiguous()
+        table = torch.full((1, WIDE), -1, dtype=torch.int32)
+        table[0, :7] = torch.arange(pool - 7, pool, dtype=torch.int32).flip(0)
         kk, vv = (torch.randn(7 * page, hkv, dim, generator=gen).half() for _ in range(2))
         k[pool - 7:] = kk.view(7, page, hkv, dim).to(DEV)
         v[pool - 7:] = vv.view(7, page, hkv, dim).to(DEV)
