@@ -692,6 +692,9 @@ class Q4Gemv:
             rope = q4gemv_rope(freqs.data_ptr(), 2 * freqs.numel(), interleaved, amp)
         if x_out is None:
             x_out = self._new((hidden,), _torch.float16, stream)
+        elif x_out.dtype is not _torch.float16 or x_out.numel() != hidden or not x_out.is_contiguous():
+            raise Q4Error(Q4_ESHAPE, f"x_out: contiguous float16 [{hidden}] expected")
+        self._on_device(x_out.get_device())
         self._check(_lib.q4gemv_run_stack_mixed(
             self.h, la, ma, len(layers), hidden, ffn, q_heads, kv_heads, rope,
             _ints(length, "length", self.device, 1), x_in.data_ptr(), x_out.data_ptr(), self._stream_of(stream)))

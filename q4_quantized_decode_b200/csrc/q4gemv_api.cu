@@ -1311,6 +1311,23 @@ int q4gemv_run_stack_mixed(q4gemv_t h, const q4gemv_layer* layers, const q4gemv_
     if (is_host_pointer(x_in) || is_host_pointer(x_out))
         return fail(h, Q4_EINVAL, "run_stack_mixed: x_in and x_out must be device memory");
     if (!aligned16(x_in) || !aligned16(x_out)) return fail(h, Q4_EALIGN, "run_stack_mixed: misaligned vector");
+    const float scale = 1.f / sqrtf((float)D);
+    auto linear = [&](const q4gemv_mixer& m) {
+        q4gemv_linattn_args a = {};
+        a.log_decay = m.log_decay;
+        a.state_in = a.state_out = m.state;
+        a.q_stride = a.k_stride = kvn;
+        a.v_stride = a.out_stride = hidden;
+        a.n_slots = 1;
+        a.qk_heads = kv_heads;
+        a.v_heads = q_heads;
+        a.k_dim = a.v_dim = D;
+        a.scale = scale;
+        a.dtype = Q4GEMV_F16;
+        return a;
+    };
+    // All layers are checked before the first one changes a cache or a state
+    // (a batch of no rows runs the mixers' checks alone).
     for (int l = 0; l < n_layers; ++l) {
         const q4gemv_layer& L = layers[l];
         const q4gemv_mixer& m = mixers[l];
@@ -1321,8 +1338,14 @@ int q4gemv_run_stack_mixed(q4gemv_t h, const q4gemv_layer* layers, const q4gemv_
         if (m.kind == Q4GEMV_MIX_ATTENTION) {
             if (m.kv.dtype != Q4GEMV_F16 || m.kv.n_heads != kv_heads || m.kv.head_dim != D)
                 return fail(h, Q4_ESHAPE, "run_stack_mixed: the cache of layer %d has other heads", l);
+            const int s = q4gemv_kv_append(h, &m.kv, 0, 0, nullptr, nullptr, nullptr, rope, nullptr, 0, 0, nullptr, kvn,
+                                           nullptr, kvn, nullptr, 0, stream);
+            if (s != Q4_OK) return s;
         } else if (m.kind == Q4GEMV_MIX_LINEAR) {
             if (!m.log_decay || !m.state) return fail(h, Q4_EINVAL, "run_stack_mixed: null state in layer %d", l);
+            const q4gemv_linattn_args a = linear(m);
+            const int s = q4gemv_linattn(h, &a, 0, 0, nullptr, 1, stream);
+            if (s != Q4_OK) return s;
         } else {
             return fail(h, Q4_EINVAL, "run_stack_mixed: unknown mixer in layer %d", l);
         }
@@ -1349,7 +1372,6 @@ int q4gemv_run_stack_mixed(q4gemv_t h, const q4gemv_layer* layers, const q4gemv_
     }
     __half* buf[6];
     for (int i = 0; i < 6; ++i) buf[i] = h->mix_act + off[i];
-    const float scale = 1.f / sqrtf((float)D);
     const __half* x = static_cast<const __half*>(x_in);
     for (int l = 0; l < n_layers; ++l) {
         const q4gemv_layer& L = layers[l];
@@ -1364,21 +1386,11 @@ int q4gemv_run_stack_mixed(q4gemv_t h, const q4gemv_layer* layers, const q4gemv_
                 rc = q4gemv_attn_paged(h, &m.kv, 1, 1, h->mix_start, len, 1, buf[1], hidden, q_heads, buf[2], hidden, scale,
                                        1, 0, stream);
         } else {
-            q4gemv_linattn_args a = {};
+            q4gemv_linattn_args a = linear(m);
             a.q = buf[0];
             a.k = buf[0] + kvn;
             a.v = buf[0] + 2 * kvn;
-            a.log_decay = m.log_decay;
-            a.state_in = a.state_out = m.state;
             a.out = buf[2];
-            a.q_stride = a.k_stride = kvn;
-            a.v_stride = a.out_stride = hidden;
-            a.n_slots = 1;
-            a.qk_heads = kv_heads;
-            a.v_heads = q_heads;
-            a.k_dim = a.v_dim = D;
-            a.scale = scale;
-            a.dtype = Q4GEMV_F16;
             rc = q4gemv_linattn(h, &a, 1, 1, h->mix_start, 1, stream);
         }
         if (rc != Q4_OK) return rc;

@@ -182,3 +182,32 @@ def test_refusals(eng):
     finally:
         eng.set_fault("none")
     assert eng.sync_status() == q4.Q4_OK
+
+
+@pytest.mark.parametrize("broken", ["table", "stride", "state"])
+def test_a_bad_layer_is_refused_before_anything_runs(eng, broken):
+    """A later layer's arguments are wrong: the first one's state stays."""
+    t = Trunk(eng, ["linear", "attention", "linear"], 256, 512, 4, 2, 101, 2)
+    x = f16_dev(synth.normal_f16(1, synth.act_id(0), 256))
+    before = t.mixers[0][1].clone()
+    if broken == "table":
+        t.mixers[1].args.table_cols = 0
+    elif broken == "stride":
+        t.mixers[1].args.token_stride += 4
+    else:
+        g, s = t.mixers[2]
+        t.mixers[2] = (g, torch.zeros(s.numel() + 1, device=DEV)[1:].view(s.shape))    # 4-byte aligned
+    with pytest.raises(q4.Q4Error):
+        t.step(eng, x, 1)
+    torch.cuda.synchronize()
+    assert torch.equal(t.mixers[0][1], before)
+    assert eng.sync_status() == q4.Q4_OK
+
+
+def test_output_is_checked(eng):
+    t = Trunk(eng, ["linear"], 256, 512, 4, 2, 102, 2)
+    x = f16_dev(synth.normal_f16(1, synth.act_id(0), 256))
+    for out in (torch.zeros(255, dtype=torch.float16, device=DEV), torch.zeros(256, device=DEV),
+                torch.zeros(512, dtype=torch.float16, device=DEV)[::2], torch.zeros(256, dtype=torch.float16)):
+        with pytest.raises(q4.Q4Error):
+            t.step(eng, x, 1, x_out=out)
