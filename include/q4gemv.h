@@ -543,7 +543,9 @@ Q4GEMV_API int q4gemv_kv_append(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, i
  *           q or the cache
  *   max_new : the most new tokens of a sequence, as far as the caller knows
  *           (1 <= max_new): it chooses the kernel, and results are right
- *           whatever it says */
+ *           whatever it says
+ * Tokens at places from 2^31 - 2^25 on are left out (Q4_EINDEX); rows times
+ * the query heads of a key head stay under 2^31 - 2^25 (Q4_ESHAPE). */
 Q4GEMV_API int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_seqs,
                                  const int32_t* start, const int32_t* len, int64_t max_new,
                                  const void* q, int64_t q_stride, int64_t q_heads, void* out,
@@ -612,8 +614,9 @@ typedef struct {
  *   x_in, x_out : device, hidden binary16 (x_out may alias x_in)
  * Launches its kernels on `stream` (4 products and 1 or 2 mixer kernels a
  * layer), so it may be captured into a graph and replayed token by token; the
- * first call with larger sizes must come outside a capture.  Errors of the
- * parts it runs; Q4_ESHAPE if q_heads does not divide hidden, kv_heads does not
+ * first call with larger sizes must come outside a capture.  Arguments of all
+ * layers are checked before anything is launched: errors of the parts it runs;
+ * Q4_ESHAPE if q_heads does not divide hidden, kv_heads does not
  * divide q_heads, or a layer's cache has other heads. */
 Q4GEMV_API int q4gemv_run_stack_mixed(q4gemv_t h, const q4gemv_layer* layers, const q4gemv_mixer* mixers,
                                       int n_layers, int64_t hidden, int64_t ffn, int64_t q_heads,

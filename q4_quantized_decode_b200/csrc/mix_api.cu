@@ -134,11 +134,17 @@ q4::RaggedArgs ragged(int64_t rows, int64_t n_seqs, const int32_t* start, const 
 // one key head of 64 over 8000 tokens 39 / 43.
 constexpr int kSplitRowsMin = 64, kSplitRowsMax = 1024;
 constexpr int64_t kSplitReads = 300000;
-// Up to this many new tokens of a sequence run token by token (us a token and
-// head-parallel step: 0.65; a chunk of up to 128 tokens costs 11).
+// Sequences of up to this many new tokens run token by token.  Measured, 40
+// heads of 128 x 128: 0.65 us a token against 11 us for a chunk of up to 128;
+// with 8 such sequences the two meet between 12 and 16 tokens.
 constexpr int kLinRecurMax = 12;
 // Chunks of a prompt's segment, at least.
 constexpr int kLinSegChunks = 4;
+
+// Places and rows of a sequence stay this far under 2^31: kernels round them up
+// to tiles, and the cost of a tensor-core unit is its first row tile's keys
+// plus up to a place for each new token (at most 2^24).
+constexpr int64_t kSlack = 1 << 25;
 
 int split_dp(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
@@ -231,6 +237,22 @@ cudaError_t setup_type() {
     return cudaSuccess;
 }
 
+// Loads a kernel now: its first launch may be in a graph's capture.
+template <typename F>
+cudaError_t load(F* kernel) {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kernel);
+}
+template <typename T>
+cudaError_t load_type() {
+    for (cudaError_t e :
+         {load(q4::kv_append_kernel<T, q4::kRopeInterleaved>), load(q4::kv_append_kernel<T, q4::kRopeHalf>),
+          load(q4::kv_append_kernel<T, q4::kRopeHalfScalar>), load(q4::lin_recur_kernel<T, 4>),
+          load(q4::lin_recur_kernel<T, 8>), load(q4::lin_recur_kernel<T, 16>)})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
+}
+
 template <typename T>
 cudaError_t append_launch(const q4::AppendArgs& a, bool interleaved, dim3 grid, cudaStream_t st) {
     if (interleaved)
@@ -242,8 +264,10 @@ cudaError_t append_launch(const q4::AppendArgs& a, bool interleaved, dim3 grid, 
 }  // namespace
 
 cudaError_t q4::mix_setup() {
-    const cudaError_t e = setup_type<__half>();
-    return e != cudaSuccess ? e : setup_type<__nv_bfloat16>();
+    for (cudaError_t e : {setup_type<__half>(), setup_type<__nv_bfloat16>(), load_type<__half>(),
+                          load_type<__nv_bfloat16>(), load(q4::lin_scan_kernel)})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
 }
 
 void q4::mix_workspace(int sms, size_t* ws_bytes, size_t* cnt_bytes) {
@@ -356,6 +380,8 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
     if (max_new < 1) return bad(h, Q4_EINVAL, call, "max_new under 1");
     if (q_heads < 1 || q_heads > Q4GEMV_MAX_HEADS || q_heads % kv->n_heads != 0)
         return bad(h, Q4_ESHAPE, call, "q_heads is not a multiple of n_heads in [1, 1024]");
+    if (rows * (q_heads / kv->n_heads) > INT32_MAX - kSlack)     // kernels count them in 32 bits
+        return bad(h, Q4_ESHAPE, call, "rows times the query heads of a key head of 2^31 - 2^25 or more");
     if (rows > 0 && (!q || !out)) return bad(h, Q4_EINVAL, call, "null pointer");
     if (!aligned(q, 16) || !aligned(out, 16)) return bad(h, Q4_EALIGN, call, "misaligned pointer");
     if (!row_stride_ok(q_stride, q_heads, kv->head_dim) || !row_stride_ok(out_stride, q_heads, kv->head_dim))
@@ -380,7 +406,7 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
     a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
     a.causal = causal ? 1 : 0;
     a.window = window > INT32_MAX ? INT32_MAX : (int)window;
-    a.cap = (int)std::min<int64_t>(kv->table_cols * kv->page_size, INT32_MAX - 4096);
+    a.cap = (int)std::min<int64_t>(kv->table_cols * kv->page_size, INT32_MAX - kSlack);
     a.err = cx.err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool f16 = kv->dtype == Q4GEMV_F16;

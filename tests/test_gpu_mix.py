@@ -20,6 +20,10 @@ Tolerances, from the arithmetic (u = half a step of the 16-bit type):
           (binary16 is given 2^-10 = 2 u, as before the operands' type was the
           tensors'; bfloat16 u = 2^-8); the same sums, and u |o| for the output.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 
 from tests import mix_ref as ref
@@ -34,6 +38,7 @@ import q4_quantized_decode_b200 as q4  # noqa: E402
 
 DTYPES = [torch.float16, torch.bfloat16]
 DEV = "cuda:0"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -468,6 +473,34 @@ def test_attend_long_context_offsets(eng):
             close(out[:, h], o, tol, f"head {h}")
 
 
+@pytest.mark.parametrize("new", [1, 200])
+def test_attend_places_near_the_end_of_32_bits(eng, new):
+    """A table of 2^31 places (one page, over and over) and a length that
+    reaches their end: what lies from place 2^31 - 2^25 on is left out and told.
+    Keys and queries are zeros, so all weights are 1 and every output is the one
+    value.  A piece (a CTA's part, at least 148 of them) has under 2^24 tokens, so
+    its sums of ones are exact, and its sums of 1.5 a tile (multiples of 8 under
+    2^25) are too; joining under 2^10 pieces in 32 bits is off by less than
+    2^-13, the output's rounding by 2^-11 of the value: 2^-10 together."""
+    page = 1 << 20
+    k = torch.zeros(1, page, 1, 8, dtype=torch.float16, device=DEV)
+    v = torch.full_like(k, 1.5)
+    cache = q4.PagedKV(k, v, torch.zeros(1, 2 ** 31 // page, dtype=torch.int32, device=DEV))
+    q = torch.zeros(new, 1, 8, dtype=torch.float16, device=DEV)
+    out = eng.attn_paged(cache, ints([0, new]), ints([2 ** 31 - 1]), q)
+    assert eng.sync_status() == q4.Q4_EINDEX
+    assert (out.float() - 1.5).abs().max().item() <= 1.5 * 2.0 ** -10
+
+
+def test_attend_more_rows_than_32_bits_are_refused(eng):
+    """2^24 rows of 1024 query heads to a key head: refused before anything is read."""
+    c = AttendCase([1], [20], 1, 1, 8, 16, torch.float16, seed=35)
+    a = c.gq.data_ptr()
+    st = q4.q4gemv_attn_paged(eng.h, c.cache.ref, 1 << 24, 1, c.start.data_ptr(), c.glen.data_ptr(), 1, a, 8192, 1024,
+                              a + 16, 8192, 1.0, 1, 0, None)
+    assert st == q4.Q4_ESHAPE and eng.sync_status() == q4.Q4_OK
+
+
 # ---- linear -----------------------------------------------------------------
 
 class LinearCase:
@@ -835,6 +868,48 @@ def test_streams(eng):
     assert eng.sync_status(side) == q4.Q4_OK
     c.check(out)
     assert torch.equal(out, out2)
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    """A process whose first launch of each kernel is in a graph's capture."""
+    code = """
+import torch, q4_quantized_decode_b200 as q4
+d = "cuda:0"
+eng = q4.Q4Gemv(0)
+gen = torch.Generator().manual_seed(1)
+t = lambda *s: torch.randn(*s, generator=gen).half().to(d)
+i = lambda *x: torch.tensor(x, dtype=torch.int32, device=d)
+f = eng.rope_freqs(64)
+q, k, v, g = t(140, 4, 64), t(140, 2, 64), t(140, 2, 64), -torch.rand(140, 2, generator=gen).to(d)
+table, start, length = i(*range(9)).view(1, 9), i(0, 140), i(140)
+
+def run(cache, state):
+    rq = eng.kv_append(cache, start, length, k, v, q=q, freqs=f)
+    o = eng.attn_paged(cache, start, length, rq, max_new=140)
+    a, _ = eng.linattn(k, k, v, g, start, state, max_new=1)
+    b, _ = eng.linattn(k, k, v, g, start, state, max_new=2000)
+    return o, a, b, cache.k, state
+
+def fresh():
+    z = torch.zeros(9, 16, 2, 64, dtype=torch.float16, device=d)
+    return q4.PagedKV(z, z.clone(), table), torch.zeros(1, 2, 64, 64, device=d)
+
+x = fresh()
+s = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(s):
+    got = run(*x)
+s.replay()
+torch.cuda.synchronize()
+want = run(*fresh())
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert eng.sync_status() == q4.Q4_OK
+del s
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 # ---- a run of them together -------------------------------------------------
