@@ -20,7 +20,20 @@
 //              keys that no row sees have to be zeros.
 // Two products of 128 x 128 x head_dim for each accumulator and tile, 16384
 // powers of two: the tensor pipe and the exponential unit need about the same
-// time, 2048 cycles for a CTA's tile at head size 128, and bound this together.
+// time, 2048 cycles for a CTA's tile at head size 128, under which the two
+// groups' chain of S, maximum, powers, P and P V takes 4400.  Measured (f16, 40
+// query and 8 key heads of 128): 4096 new tokens behind 12288, 1.20 ms, 1000
+// TFLOP/s; four prompts' chunks of up to 1024 (bf16, 16 / 4 heads of 64, pages
+// of 24) 196 us, 346 TFLOP/s.  Part of the powers by a polynomial of degree 4 on
+// the FMA units was slower (a quarter of them: 2.30 against 2.20 ms): the
+// issue slots are as busy.
+//
+// Head sizes over 128 leave room for the sums of one accumulator beside S (256
+// and 128 of 512 columns): units of 128 rows, of which the two groups take 64
+// keys of a tile and half of the sums' columns each; a warp and its fellow of
+// the other group meet once a tile, to agree on the row maxima.  Measured, 32 /
+// 4 heads of 256: 4096 new tokens behind 8192, 1.45 ms, 946 TFLOP/s; 16 / 4
+// heads, 2048 behind 2048, 168 us (16 rows at a time on mma.sync: 1924).
 //
 // The units' key tiles are cut over the CTAs on the device: with few units
 // each is split over several CTAs, with many the units' costs (which grow with
@@ -42,27 +55,28 @@
 
 namespace q4 {
 
-constexpr int kTaRows = 256;                 // rows of a unit
 constexpr int kTaKeys = 128;                 // keys of a tile
 constexpr int kTaLoaders = 2;
 constexpr int kTaThreads = 32 * 12;
-constexpr int kTaLag = 2;                    // copies in flight behind the newest
 constexpr int kTaSegs = 4;                   // parts told ahead
 constexpr int kTaOver = 128;                 // a unit's fixed cost in keys: its start and end
 
 // Ring slots (a K or a V tile each) beside the queries.
-__host__ __device__ constexpr int ta_slots(int dp) { return dp == 64 ? 8 : 4; }
+__host__ __device__ constexpr int ta_slots(int dp) { return dp == 64 ? 8 : dp == 128 ? 4 : 2; }
+// Rows of a unit, 128 for each accumulator.
+__host__ __device__ constexpr int ta_rows(int dp) { return dp == 256 ? 128 : 256; }
 __host__ __device__ constexpr int ta_smem(int dp) {
-    return 1024 + kTaRows * dp * 2 + ta_slots(dp) * kTaKeys * dp * 2 + 512;
+    return 1024 + ta_rows(dp) * dp * 2 + ta_slots(dp) * kTaKeys * dp * 2 + 512 + (dp == 256 ? 2 * 2 * 128 * 4 : 0);
 }
-// Floats of a workspace slot: sums [dp / 4][256][4], maxima, weights' sums.
-__host__ __device__ constexpr int ta_slot(int dp) { return kTaRows * (dp + 2); }
+// Floats of a workspace slot: sums [dp / 4][rows][4], maxima, weights' sums.
+__host__ __device__ constexpr int ta_slot(int dp) { return ta_rows(dp) * (dp + 2); }
 
 struct TcAttnArgs {
     AttnArgs a;
     float* ws;           // [2 * gridDim.x] slots
     int* cnt;            // [gridDim.x] arrivals, zero between calls
     int min_rows;        // sequences of at most this many rows are another kernel's
+    int rows;            // of a unit
     uint32_t idesc_s, idesc_o;
     int box;             // tokens of a tensor-map box (8..128, dividing page_size), 0: no maps
     CUtensorMap kmap, vmap;   // [page][head][token][element], boxes of 64 elements x `box` tokens
@@ -82,11 +96,11 @@ __device__ __forceinline__ TaSeq ta_seq(const TcAttnArgs& g, int s) {
     const int64_t rows = (int64_t)q.n * g.a.group;
     q.tiles = q.c0 = q.c1 = 0;
     if (rows <= g.min_rows) return q;
-    q.tiles = (int)((rows + kTaRows - 1) / kTaRows);
+    q.tiles = (int)((rows + g.rows - 1) / g.rows);
     int lo, hi;
     if (g.a.causal && (g.a.window == 0 || g.a.window >= q.len)) {
-        seen_range(g.a, q.len, q.n, min(q.n - 1, (kTaRows - 1) / g.a.group), lo, hi);
-        q.c1 = kTaRows / g.a.group;
+        seen_range(g.a, q.len, q.n, min(q.n - 1, (g.rows - 1) / g.a.group), lo, hi);
+        q.c1 = g.rows / g.a.group;
     } else {
         seen_range(g.a, q.len, q.n, q.n - 1, lo, hi);
     }
@@ -169,8 +183,8 @@ __device__ __forceinline__ void ta_unit(const TaSeq& q, int nh, int64_t x, int& 
 // Keys of row tile rt (the first row starts lowest, the last ends highest):
 // the first 128-key tile's first key, the tiles.
 __device__ __forceinline__ int ta_tiles(const TcAttnArgs& g, const TaSeq& q, int rt, int& tlo, int& thi, int& base) {
-    const int t0 = (int)div_floor((int64_t)rt * kTaRows, g.a.group);
-    const int t1 = min(q.n - 1, (int)div_floor((int64_t)(rt + 1) * kTaRows - 1, g.a.group));
+    const int t0 = (int)div_floor((int64_t)rt * g.rows, g.a.group);
+    const int t1 = min(q.n - 1, (int)div_floor((int64_t)(rt + 1) * g.rows - 1, g.a.group));
     int lo1, hi0;
     seen_range(g.a, q.len, q.n, t0, tlo, hi0);
     seen_range(g.a, q.len, q.n, t1, lo1, thi);
@@ -312,9 +326,9 @@ __device__ __forceinline__ void ta_next(const TcAttnArgs& g, TaWalk& w, TaSeg& e
     e.len = w.q.len;
     e.n = w.q.n;
     e.first = w.q.first;
-    e.n_rows = (int)min((int64_t)kTaRows, (int64_t)w.q.n * g.a.group - (int64_t)rt * kTaRows);
-    e.t0 = (int)div_floor((int64_t)rt * kTaRows, g.a.group);
-    e.g0 = (int)((int64_t)rt * kTaRows - (int64_t)e.t0 * g.a.group);
+    e.n_rows = (int)min((int64_t)g.rows, (int64_t)w.q.n * g.a.group - (int64_t)rt * g.rows);
+    e.t0 = (int)div_floor((int64_t)rt * g.rows, g.a.group);
+    e.g0 = (int)((int64_t)rt * g.rows - (int64_t)e.t0 * g.a.group);
     e.j0 = base + i0 * kTaKeys;
     e.nt = i1 - i0;
 }
@@ -329,17 +343,35 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
                  : "memory");
 }
 
+// Whether both warps of pair `pair` (64 threads) are well; they meet here.
+__device__ __forceinline__ bool pair_ok(int pair, bool ok) {
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.cta.red.and.pred q, %2, 64, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all) : "r"((uint32_t)ok), "r"(2 + pair) : "memory");
+    return all != 0;
+}
+
 template <typename T, int DP>
 __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnArgs g) {
     constexpr int NS = ta_slots(DP);
     constexpr int CH = DP / 8;
     constexpr uint32_t kHalf = kTaKeys * 128;            // one 64-element part of a 128-row tile
     constexpr uint32_t kTile = kHalf * (DP / 64);
+    constexpr int ROWS = ta_rows(DP), NA = ROWS / 128;   // accumulators
+    // One accumulator: the two groups of softmax warps share its rows, 64 keys
+    // of a tile and half of the output's columns each.
+    constexpr bool kPair = NA == 1;
+    constexpr int NV = kPair ? 64 : 128;                 // scores of a thread
+    constexpr int DO = kPair ? DP / 2 : DP;              // output columns of a thread
+    constexpr int kLag = NS > 2 ? 2 : 1;                 // copies in flight behind the newest
     constexpr uint32_t kColO = 256;                      // TMEM columns: S at 0 and 128, sums from 256
     extern __shared__ uint8_t ta_raw[];
     const uint32_t raw0 = smem_addr(ta_raw);
-    const uint32_t sQ = (raw0 + 1023u) & ~1023u;         // two tiles of 128 rows
-    const uint32_t sRing = sQ + 2 * kTile;
+    const uint32_t sQ = (raw0 + 1023u) & ~1023u;         // NA tiles of 128 rows
+    const uint32_t sRing = sQ + NA * kTile;
     uint64_t* full = reinterpret_cast<uint64_t*>(ta_raw + (sRing - raw0) + NS * kTile);   // [NS]
     uint64_t* empty = full + NS;                         // [NS]
     uint64_t* qfull = empty + NS;                        // queries in place
@@ -355,6 +387,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
     volatile int* never = abort_flag + 1;                // stays 0
     volatile int* last_word = abort_flag + 2;
     volatile int* odd = abort_flag + 3;                  // [16] of the pieces with keys, in order: take it row by row
+    float* meet = reinterpret_cast<float*>(ta_raw + (sRing - raw0) + NS * kTile + 512);   // [2][2][128], kPair
 
     const AttnArgs& a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -369,7 +402,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
         for (int i = 0; i < 2; ++i) {
             mbar_init(sfull + i, 1);
             mbar_init(pfull + i, 4);
-            mbar_init(phalf + i, 4);
+            mbar_init(phalf + i, kPair ? 8 : 4);
             mbar_init(ofull + i, 1);
         }
         for (int i = 0; i < 16; ++i) odd[i] = 0;
@@ -556,9 +589,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                         look |= 1u << (u & 7);
                         mark = (mark & ~(15u << (4 * (u & 7)))) | ((uint32_t)(seg_no & 15) << (4 * (u & 7)));
                     }
-                    if (u + 1 > told + kTaLag) {
-                        cp_async_wait<kTaLag>();
-                        signal(u + 1 - kTaLag);
+                    if (u + 1 > told + kLag) {
+                        cp_async_wait<kLag>();
+                        signal(u + 1 - kLag);
                     }
                 }
             }
@@ -616,14 +649,14 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 wait(full + u % NS, (u / NS) & 1);
                 if (ok) {
                     scores(0, u % NS);
-                    scores(1, u % NS);
+                    if (NA > 1) scores(1, u % NS);
                     tc_commit(empty + u % NS);
                 }
                 for (int i = 0; i < nt && ok; ++i) {
                     const uint32_t uv = u + 1, uk = u + 2;
                     wait(full + uv % NS, (uv / NS) & 1);
 #pragma unroll
-                    for (int acc = 0; acc < 2; ++acc) {
+                    for (int acc = 0; acc < NA; ++acc) {
                         auto weighted = [&](int kk) {
                             tc_mma_f16_ta(tmem + kColO + 128u * acc, tmem + 128u * acc + 8u * kk,
                                           tc_sdesc_sw128_nmajor(sRing + (uv % NS) * kTile + 2048u * kk, kHalf),
@@ -638,14 +671,14 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                         if (ok) {
 #pragma unroll
                             for (int kk = kTaKeys / 32; kk < kTaKeys / 16; ++kk) weighted(kk);
-                            if (acc == 1) tc_commit(empty + uv % NS);
+                            if (acc == NA - 1) tc_commit(empty + uv % NS);
                             if (i + 1 == nt) tc_commit(ofull + acc);
                         }
                         if (i + 1 < nt) {
                             if (acc == 0) wait(full + uk % NS, (uk / NS) & 1);
                             if (ok) {
                                 scores(acc, uk % NS);
-                                if (acc == 1) tc_commit(empty + uk % NS);
+                                if (acc == NA - 1) tc_commit(empty + uk % NS);
                             }
                         }
                     }
@@ -665,10 +698,13 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        // ---- softmax: a thread has row `row` of accumulator `acc` ----
-        const int acc = warp >> 2, row = threadIdx.x & 127;
+        // ---- softmax: a thread has row `row` of accumulator `acc`, or the part
+        // `part` of the one accumulator's row: keys 64 part .. + 64, columns
+        // 128 part .. + 128 ----
+        const int grp = warp >> 2, acc = kPair ? 0 : grp, part = kPair ? grp : 0, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t tS = tmem + lanes + 128u * acc, tO = tmem + lanes + kColO + 128u * acc;
+        const uint32_t tS = tmem + lanes + 128u * acc + 64u * part, tO = tmem + lanes + kColO + 128u * grp;
+        const uint32_t tP = tmem + lanes + 128u * acc + 32u * part;
         uint32_t ns = 0;                                 // S's waited for
         int q_no = 0;                                    // pieces with keys
         bool ok = true;
@@ -682,12 +718,14 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
             const TaSeg& e = segs[part_no % kTaSegs];
             if (!e.more) break;
             const int xr = acc * 128 + row;              // of the unit's rows
+            const int cb = part * DO;                    // first output column
             if (e.nt > 0) {
                 // Queries of this accumulator: a thread's chunk of every
-                // 128 / CH-th row.
-                const int ch = (int)(threadIdx.x & 127) % CH;
+                // kHands / CH-th row.
+                constexpr int kHands = kPair ? 256 : 128;    // threads of an accumulator's queries
+                const int hand = (int)threadIdx.x % kHands, ch = hand % CH;
 #pragma unroll 4
-                for (int rr = (int)(threadIdx.x & 127) / CH; rr < 128; rr += 128 / CH) {
+                for (int rr = hand / CH; rr < 128; rr += kHands / CH) {
                     const int x = acc * 128 + rr, gx = e.g0 + x, t = gx / a.group, gh = gx - t * a.group;
                     const bool in = x < e.n_rows && 8 * ch < D;
                     const T* src = static_cast<const T*>(a.q) +
@@ -719,24 +757,24 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
             for (int i = 0; i < e.nt && ok; ++i) {
                 ok = __all_sync(0xFFFFFFFFu, tc_wait_long(sfull + acc, ns & 1, abort_flag));
                 ++ns;
-                if (!ok) break;
+                if (!kPair && !ok) break;                // (a pair ends together)
                 tc_fence_after();
-                float v[4][32];                          // the row's 128 scores
+                float v[NV / 32][32];                    // the row's scores (its part's)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) tc_ld32(tS + 32u * x, v[x]);
+                for (int x = 0; x < NV / 32; ++x) tc_ld32(tS + 32u * x, v[x]);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) tc_wait_ld(v[x]);
+                for (int x = 0; x < NV / 32; ++x) tc_wait_ld(v[x]);
                 const int j = e.j0 + i * kTaKeys;
                 if (neg || flat) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int x = 0; x < NV / 32; ++x)
 #pragma unroll
                         for (int y = 0; y < 32; ++y) v[x][y] = neg ? -v[x][y] : 0.f * v[x][y];
                 }
                 if (j < wlo || j + kTaKeys > whi) {
-                    const int c0 = lo - j, c1 = hi - j;
+                    const int c0 = lo - j - 64 * part, c1 = hi - j - 64 * part;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int x = 0; x < NV / 32; ++x)
 #pragma unroll
                         for (int y = 0; y < 32; ++y)
                             if (32 * x + y < c0 || 32 * x + y >= c1) v[x][y] = -INFINITY;
@@ -746,10 +784,21 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 for (int x = 0; x < 8; ++x) {
                     mx[x] = v[0][x];
 #pragma unroll
-                    for (int y = 8; y < 128; y += 8) mx[x] = fmaxf(mx[x], v[(x + y) >> 5][(x + y) & 31]);
+                    for (int y = 8; y < NV; y += 8) mx[x] = fmaxf(mx[x], v[(x + y) >> 5][(x + y) & 31]);
                 }
-                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sc;
+                float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sc;
+                if (kPair) {
+                    // The row's other part, read as well by now: P may go into
+                    // S's place.
+                    float* mt = meet + 256 * (ns & 1);
+                    mt[128 * part + row] = top;
+                    tc_fence_before();
+                    ok = pair_ok(warp & 3, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    top = fmaxf(mt[row], mt[128 + row]);
+                }
                 float f = 1.f;
                 if (i == 0) {
                     m = top;
@@ -761,7 +810,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 if (__any_sync(0xFFFFFFFFu, f != 1.f)) {
                     // S came after the last P V, so the sums are at rest.
 #pragma unroll 1
-                    for (int x = 0; x < DP / 16; ++x) {
+                    for (int x = 0; x < DO / 16; ++x) {
                         uint32_t o[16];
                         tc_ld16(tO + 16u * x, o);
 #pragma unroll
@@ -769,11 +818,17 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                         tc_st16(tO + 16u * x, o);
                     }
                 }
+                if (kPair && part == 1) {                // its columns are ready for the product
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(phalf + acc);
+                }
                 const float mu = m == -INFINITY ? 0.f : m;
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < NV / 32; ++x) {
                     uint32_t pw[16];
 #pragma unroll
                     for (int y = 0; y < 16; ++y) {
@@ -783,8 +838,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                         sum[y & 1] = fadd2(sum[y & 1], t);
                         pw[y] = Elem<T>::pack(t.x, t.y);
                     }
-                    tc_st16(tS + 16u * x, pw);
-                    if (x == 1) {
+                    tc_st16(tP + 16u * x, pw);
+                    if (!kPair && x == 1) {
                         // The first 64 keys' weights: their product may begin.
                         tc_wait_st();
                         tc_fence_before();
@@ -796,11 +851,17 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(pfull + acc);
+                if (lane == 0) mbar_arrive((kPair && part == 0 ? phalf : pfull) + acc);
             }
             if (ok && e.nt > 0) {
                 ok = __all_sync(0xFFFFFFFFu, tc_wait_long(ofull + acc, (q_no - 1) & 1, abort_flag));
                 tc_fence_after();
+            }
+            if (kPair) {                                 // the row's weights, both parts'
+                float* mt = meet + 256 * ((ns + 1) & 1);
+                mt[128 * part + row] = l;
+                ok = pair_ok(warp & 3, ok);
+                l = mt[row] + mt[128 + row];
             }
             // The copying warps' marks on this piece reach here through the
             // products' barriers; they are at most five pieces ahead.
@@ -810,7 +871,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 if (!rows_apart) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-                    for (int x = 0; x < DP / 32; ++x) {
+                    for (int x = 0; x < DO / 32; ++x) {
                         float o[32];
                         if (e.nt > 0) {
                             tc_ld32(tO + 32u * x, o);
@@ -821,7 +882,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                             float v[8];
 #pragma unroll
                             for (int z = 0; z < 8; ++z) v[z] = e.nt > 0 ? o[8 * y + z] * inv : 0.f;
-                            if (real && 32 * x + 8 * y < D) *reinterpret_cast<uint4*>(out + 32 * x + 8 * y) = pack8<T>(v);
+                            if (real && cb + 32 * x + 8 * y < D)
+                                *reinterpret_cast<uint4*>(out + cb + 32 * x + 8 * y) = pack8<T>(v);
                         }
                     }
                 }
@@ -831,19 +893,21 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 // weights' sum of -1.
                 const int rr = xr;
 #pragma unroll
-                for (int x = 0; x < DP / 32; ++x) {
+                for (int x = 0; x < DO / 32; ++x) {
                     float o[32];
                     if (e.nt > 0) {
                         tc_ld32(tO + 32u * x, o);
                         tc_wait_ld(o);
 #pragma unroll
                         for (int y = 0; y < 8; ++y)
-                            *reinterpret_cast<float4*>(slot + ((8 * x + y) * kTaRows + rr) * 4) =
+                            *reinterpret_cast<float4*>(slot + ((cb / 4 + 8 * x + y) * ROWS + rr) * 4) =
                                 make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                     }
                 }
-                slot[kTaRows * DP + rr] = m;
-                slot[kTaRows * DP + kTaRows + rr] = rows_apart ? -1.f : l;
+                if (part == 0) {
+                    slot[ROWS * DP + rr] = m;
+                    slot[ROWS * DP + ROWS + rr] = rows_apart ? -1.f : l;
+                }
                 __threadfence();
                 bar_first256();
                 if (threadIdx.x == 0) *last_word = atom_add_acq_rel_gpu(g.cnt + e.c_lo, 1) == e.pieces - 1;
@@ -859,23 +923,23 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                 auto piece = [&](int p) {
                     return g.ws + (int64_t)(p ? 2 * (e.c_lo + p) : e.slot0) * ta_slot(DP) + xr * 4;
                 };
-                constexpr int kM = kTaRows * DP;         // maxima, then sums
+                constexpr int kM = ROWS * DP;         // maxima, then sums
                 float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
                 for (int p = 0; p < e.pieces; ++p) {
                     const float* sp = piece(p) - 3 * xr + kM;
                     top = fmaxf(top, __ldcg(sp));
-                    if (__ldcg(sp + kTaRows) == -1.f) apart = true;
+                    if (__ldcg(sp + ROWS) == -1.f) apart = true;
                 }
                 const float mu = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
                 for (int p = 0; p < e.pieces; ++p) {
                     const float* sp = piece(p) - 3 * xr + kM;
-                    sum += exp2f(__ldcg(sp) - mu) * __ldcg(sp + kTaRows);
+                    sum += exp2f(__ldcg(sp) - mu) * __ldcg(sp + ROWS);
                 }
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
-                for (int x = 0; x < DP / 64; ++x) {
+                for (int x = 0; x < DO / 64; ++x) {
                     float4 o[16];
 #pragma unroll
                     for (int y = 0; y < 16; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -886,7 +950,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                         float4 v[16];
 #pragma unroll
                         for (int y = 0; y < 16; ++y)
-                            v[y] = __ldcg(reinterpret_cast<const float4*>(sp + (16 * x + y) * (4 * kTaRows)));
+                            v[y] = __ldcg(reinterpret_cast<const float4*>(sp + (cb / 4 + 16 * x + y) * (4 * ROWS)));
                         if (wt == 0.f) continue;         // no keys: the slot's sums were not written
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
@@ -899,8 +963,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
                     if (real)
 #pragma unroll
                         for (int y = 0; y < 16; ++y)
-                            if (64 * x + 4 * y < D)
-                                *reinterpret_cast<uint2*>(out + 64 * x + 4 * y) =
+                            if (cb + 64 * x + 4 * y < D)
+                                *reinterpret_cast<uint2*>(out + cb + 64 * x + 4 * y) =
                                     make_uint2(Elem<T>::pack(o[y].x * inv, o[y].y * inv),
                                                Elem<T>::pack(o[y].z * inv, o[y].w * inv));
                 }

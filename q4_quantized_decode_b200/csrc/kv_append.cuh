@@ -11,7 +11,10 @@
 // It moves each byte of q, k and v once in and once out and is bound by that.
 // A thread keeps one place within the head (a pair of 16-byte chunks in the
 // half layout, one chunk in the interleaved one), takes its eight angles once
-// and walks over the heads with them, so nothing goes through shared memory.
+// and walks over the heads with them, so nothing goes through shared memory;
+// 64 threads a row keep 32 rows in flight on an SM.  Measured (40 query, 8 key
+// heads of 128, f16): six prompts of up to 2048 tokens, 39 us, 5.2 TB/s; one
+// token 3.0 us, 48 tokens far out (heads of 256, 64 of it rotated) 5.5.
 #pragma once
 
 #include "mix_common.cuh"

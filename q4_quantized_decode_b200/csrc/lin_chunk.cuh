@@ -11,7 +11,9 @@
 // value columns have their sums of O^T over their halves of k_dim and of the
 // tokens, and exchange half of them through shared memory; with half the state
 // each, 16 warps have room on an SM, which the products' latencies need (with 8
-// warps of the whole k_dim a scheduler issued in 38 of 100 cycles).
+// warps of the whole k_dim a scheduler issued in 38 of 100 cycles).  Measured,
+// 8192 tokens of 40 heads of 256 x 256: 1.94 ms (f16), 2.17 (bf16), 44 and 40
+// TFLOP/s of the recurrence's products.
 //
 // The next chunk's rows are copied, and its decays summed, while this one's
 // products run, and each thread looks over the magnitudes of what it copied

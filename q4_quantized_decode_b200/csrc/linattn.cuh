@@ -28,7 +28,8 @@ struct LinArgs {
 // A CTA keeps 32 columns of one head's state in registers and walks over the
 // sequence's new tokens.  A single token is bound by the state's way in and
 // out: each thread has all its rows' loads in flight at once, and a warp's
-// load covers four rows of 128 contiguous bytes.
+// load covers four rows of 128 contiguous bytes.  Measured (40 heads of 128 x
+// 128): 96 sequences' tokens 82 us, 6.2 TB/s of states; one sequence's 3.0 us.
 constexpr int kLinCols = 32;
 constexpr int kLinThreads = 128;
 constexpr int kLinRowGroups = kLinThreads / (kLinCols / 4);

@@ -131,9 +131,11 @@ q4::RaggedArgs ragged(int64_t rows, int64_t n_seqs, const int32_t* start, const 
 // tokens, by the table's capacity) under kSplitReads.  Measured (us, that
 // kernel / the tensor-core one): 320 rows of 8 key heads of 128 over 1000 tokens
 // 32 / 36, 640 rows 48 / 36; 80 rows over 30000 tokens 111 / 90; 1024 rows of
-// one key head of 64 over 8000 tokens 39 / 43.
+// one key head of 64 over 8000 tokens 39 / 43.  With head sizes over 128 a read
+// costs that kernel more: 512 rows of 4 key heads of 256 over 1000 tokens 60 /
+// 38, 128 rows 36 / 38; 512 rows over none 13 / 17, 1024 rows 33 / 20.
 constexpr int kSplitRowsMin = 64, kSplitRowsMax = 1024;
-constexpr int64_t kSplitReads = 300000;
+constexpr int64_t kSplitReads = 300000, kSplitReadsWide = 60000;
 // Sequences of up to this many new tokens run token by token.  Measured, 40
 // heads of 128 x 128: 0.65 us a token against 11 us for a chunk of up to 128;
 // with 8 such sequences the two meet between 12 and 16 tokens.
@@ -210,9 +212,11 @@ bool row_map(CUtensorMap* map, const void* base, int dtype, int64_t dim, int64_t
 
 template <typename T>
 cudaError_t tc_launch(const q4::TcAttnArgs& g, int sms, cudaStream_t st) {
-    return g.a.kv.head_dim <= 64
-               ? launch(q4::attn_tc_kernel<T, 64>, dim3((unsigned)sms), q4::kTaThreads, q4::ta_smem(64), st, g)
-               : launch(q4::attn_tc_kernel<T, 128>, dim3((unsigned)sms), q4::kTaThreads, q4::ta_smem(128), st, g);
+    const dim3 grid((unsigned)sms);
+    const int dp = split_dp(g.a.kv.head_dim);
+    return dp == 64 ? launch(q4::attn_tc_kernel<T, 64>, grid, q4::kTaThreads, q4::ta_smem(64), st, g)
+         : dp == 128 ? launch(q4::attn_tc_kernel<T, 128>, grid, q4::kTaThreads, q4::ta_smem(128), st, g)
+                     : launch(q4::attn_tc_kernel<T, 256>, grid, q4::kTaThreads, q4::ta_smem(256), st, g);
 }
 template <typename T, int DP>
 cudaError_t tc_setup() {
@@ -227,6 +231,7 @@ template <typename T>
 cudaError_t setup_type() {
     for (cudaError_t e :
          {split_setup<T, 64>(), split_setup<T, 128>(), split_setup<T, 256>(), tc_setup<T, 64>(), tc_setup<T, 128>(),
+          tc_setup<T, 256>(),
           smem_limit(q4::lin_chunk_kernel<T, 256, 4, true>, q4::lc_smem(256, 4, true)),
           smem_limit(q4::lin_chunk_kernel<T, 256, 4, false>, q4::lc_smem(256, 4, false)),
           smem_limit(q4::lin_tc_kernel<T, 64, true>, q4::lt_smem(64, true)),
@@ -277,7 +282,7 @@ void q4::mix_workspace(int sms, size_t* ws_bytes, size_t* cnt_bytes) {
         floats = std::max(floats, 2 * n * q4::split_slot(dp));
         ctas = std::max(ctas, n);
     }
-    floats = std::max(floats, 2 * (size_t)sms * q4::ta_slot(128));
+    floats = std::max(floats, 2 * (size_t)sms * std::max(q4::ta_slot(128), q4::ta_slot(256)));
     *ws_bytes = floats * sizeof(float);
     *cnt_bytes = ctas * sizeof(int);
 }
@@ -414,8 +419,9 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
     // to the tensor-core kernel, those with few to the other; a batch that may
     // hold both runs both.
     const int64_t reads = kv->n_heads * n_seqs * (int64_t)a.cap;     // of one tile of each sequence
-    const int limit = (int)std::max<int64_t>(kSplitRowsMin, std::min<int64_t>(kSplitRowsMax, 16 * (kSplitReads / reads)));
-    const bool many = kv->head_dim <= 128 && max_new > limit / a.group;
+    const int64_t most = kv->head_dim > 128 ? kSplitReadsWide : kSplitReads;
+    const int limit = (int)std::max<int64_t>(kSplitRowsMin, std::min<int64_t>(kSplitRowsMax, 16 * (most / reads)));
+    const bool many = max_new > limit / a.group;
     const bool few = !many || n_seqs > 1;
     if (many) {
         q4::TcAttnArgs g;
@@ -423,7 +429,8 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
         g.ws = cx.attn_ws;
         g.cnt = cx.attn_cnt;
         g.min_rows = few ? limit : 0;
-        const int dp = kv->head_dim <= 64 ? 64 : 128;
+        const int dp = split_dp(kv->head_dim);
+        g.rows = q4::ta_rows(dp);
         // Boxes of the largest power of two of tokens that divides a page, up
         // to a tile; under 8 they would be more than the 16-byte copies' work.
         g.box = (int)std::min<int64_t>(kv->page_size & -kv->page_size, q4::kTaKeys);

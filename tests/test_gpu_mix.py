@@ -473,6 +473,44 @@ def test_attend_long_context_offsets(eng):
             close(out[:, h], o, tol, f"head {h}")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim,page", [(136, 16), (200, 24), (256, 5), (256, 64), (256, 1024)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 90), (False, 0), (False, 33)])
+def test_attend_chunks_of_wide_heads(eng, dtype, dim, page, causal, window):
+    """Head sizes past 128 on the tensor-core kernel: units of 128 rows, whole
+    and in pieces, of ragged sequences."""
+    c = AttendCase([70, 0, 301, 129], [70, 9, 640, 2500], 4, 2, dim, page, dtype, seed=dim + page, cols=WIDE,
+                   head_major=page == 64)
+    out = c.run(eng, max_new=301, causal=causal, window=window)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(out, causal=causal, window=window)
+    assert torch.equal(out, c.run(eng, max_new=301, causal=causal, window=window))
+
+
+@pytest.mark.parametrize("scale", [None, 0.0, -0.02, 3.0])
+def test_attend_wide_heads_large_scores(eng, scale):
+    for new, length in ((140, 600), (1000, 1400)):
+        c = AttendCase([new], [length], 3, 1, 256, 16, torch.float16, seed=new, amp=30.0, cols=WIDE)
+        c.check(c.run(eng, scale=scale), scale=scale)
+    assert eng.sync_status() == q4.Q4_OK
+
+
+def test_attend_wide_heads_bad_pages(eng):
+    c = AttendCase([150, 150], [400, 300], 4, 2, 256, 16, torch.float16, seed=17, cols=WIDE)
+    c.cache.table[0, 3] = 10 ** 6
+    out = c.run(eng)
+    assert eng.sync_status() == q4.Q4_EINDEX
+    assert torch.isfinite(out).all()
+    c.check(out, seqs=[1])
+    keep = torch.cat((torch.arange(48), torch.arange(64, 400)))
+    for h in range(4):
+        k, v = (ref.gather(x, c.table, 0, 400, h // 2) for x in (c.k, c.v))
+        o, a, mags = ref.attend(c.q[:150, h], k[keep], v[keep], 400 - 150 - 16, 1 / 16)
+        tol = (2.0 ** -11 + 512 * 2.0 ** -23 * mags[:, None] + 2.0 ** -18) * a + 400 * 2.0 ** -25 * 6 + \
+            2.0 ** -11 * o.abs() + 2.0 ** -25
+        close(out[:150, h], o, tol, "without the bad page")
+
+
 @pytest.mark.parametrize("new", [1, 200])
 def test_attend_places_near_the_end_of_32_bits(eng, new):
     """A table of 2^31 places (one page, over and over) and a length that
