@@ -110,6 +110,14 @@ __device__ __forceinline__ void lt_decays(float4 g, float* out) {
     }
 }
 
+// max(m, |v.x|, |v.y|); a NaN is passed over.
+__device__ __forceinline__ float max_abs(float m, float2 v) {
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(v.x), "f"(v.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 template <typename T, int DK, bool OUT>
 __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_constant__ LinTcArgs ta) {
     constexpr bool kHalf16 = Elem<T>::kExpMask == Elem<__half>::kExpMask;
@@ -387,10 +395,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             if (spoilt)
 #pragma unroll
                 for (int y = 0; y < CW; ++y) sv[y] = 0x7FFFFFFFu;
+            auto pair = [&](int y) { return make_float2(__uint_as_float(sv[y]), __uint_as_float(sv[y + 1])); };
             if (OUT && kHalf16) {
                 float m = 0.f;
 #pragma unroll
-                for (int y = 0; y < CW; ++y) m = fmaxf(m, fabsf(__uint_as_float(sv[y])));
+                for (int y = 0; y < CW; y += 2) m = max_abs(m, pair(y));
                 sx[128 * hc + row] = m;
             }
             bar();
@@ -410,17 +419,24 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             if (OUT) {
 #pragma unroll
                 for (int x = 0; x < CW / 8; ++x) {
-                    float v[8];
+                    uint32_t w[4];
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(sv[8 * x + y]) * rp;
+                    for (int y = 0; y < 4; ++y) {
+                        const float2 v = fmul2(pair(8 * x + 2 * y), both(rp));
+                        w[y] = Elem<T>::pack(v.x, v.y);
+                    }
                     const int ch = hc * (CW / 8) + x;    // 16-byte chunk of the row
                     sts128(sS + (uint32_t)(ch >> 3) * kLtHalf + (uint32_t)(row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
-                           pack8<T>(v));
+                           make_uint4(w[0], w[1], w[2], w[3]));
                 }
                 fence_proxy_async_smem();
             }
 #pragma unroll
-            for (int y = 0; y < CW; ++y) sv[y] = __float_as_uint(__uint_as_float(sv[y]) * decay * f1);
+            for (int y = 0; y < CW; y += 2) {
+                const float2 v = fmul2(fmul2(pair(y), both(decay)), both(f1));
+                sv[y] = __float_as_uint(v.x);
+                sv[y + 1] = __float_as_uint(v.y);
+            }
             store_state(sv);
             tc_fence_before();
             E = sk;
@@ -431,10 +447,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             wait(vfull, c);
             {
                 constexpr int N = (int)(2 * kLtHalf / 16) / kLtPass;
-                bool odd = n < C;
+                uint32_t top = 0;
 #pragma unroll
-                for (int x = 0; x < N; ++x) odd |= any_nonfinite<T>(lds128(sV + 16u * (tid + x * kLtPass)));
-                if (odd) {
+                for (int x = 0; x < N; ++x) top = max_abs8(top, lds128(sV + 16u * (tid + x * kLtPass)));
+                if (n < C || (top & 0xFFFFu) >= Elem<T>::kExpMask || top >> 16 >= Elem<T>::kExpMask) {
                     for (int x = tid; x < (int)(2 * kLtHalf / 16); x += kLtPass) {
                         const int r = (x >> 3) & 127;
                         const uint4 v = lds128(sV + 16u * x);
@@ -467,21 +483,32 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                 tc_wait_ld(p);
                 float m = 0.f;
                 if (hc <= (warp & 3)) {                  // else wholly above the diagonal
-                    const float bh = dec[row], bl = dec[C + row];
+                    const float2 bh = both(dec[row]), bl = both(dec[C + row]), less = both(-1.f);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         const float4 h4 = *reinterpret_cast<const float4*>(dec + 32 * hc + 4 * x);
                         const float4 l4 = *reinterpret_cast<const float4*>(dec + C + 32 * hc + 4 * x);
-                        const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
+                        const float2 hj[2] = {make_float2(h4.x, h4.y), make_float2(h4.z, h4.w)};
+                        const float2 lj[2] = {make_float2(l4.x, l4.y), make_float2(l4.z, l4.w)};
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            float d = (bh - hj[y]) + (bl - lj[y]);
-                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(d));
-                            float& v = p[4 * x + y];
-                            v = 32 * hc + 4 * x + y <= row ? v * d : 0.f;
-                            m = fmaxf(m, fabsf(v));
+                        for (int y = 0; y < 2; ++y) {
+                            float2 d = fadd2(ffma2(hj[y], less, bh), ffma2(lj[y], less, bl));
+                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d.x) : "f"(d.x));
+                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d.y) : "f"(d.y));
+                            const int at = 4 * x + 2 * y;
+                            const float2 v = fmul2(make_float2(p[at], p[at + 1]), d);
+                            p[at] = v.x;
+                            p[at + 1] = v.y;
                         }
                     }
+                    if (hc == (warp & 3)) {              // on the diagonal
+#pragma unroll
+                        for (int y = 0; y < 32; ++y)
+                            if (y > lane) p[y] = 0.f;
+                    }
+                    if (kHalf16)
+#pragma unroll
+                        for (int y = 0; y < 32; y += 2) m = max_abs(m, make_float2(p[y], p[y + 1]));
                 } else {
 #pragma unroll
                     for (int y = 0; y < 32; ++y) p[y] = 0.f;
@@ -500,7 +527,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                 }
                 uint32_t w[16];
 #pragma unroll
-                for (int y = 0; y < 16; ++y) w[y] = Elem<T>::pack(p[2 * y] * tp, p[2 * y + 1] * tp);
+                for (int y = 0; y < 16; ++y) {
+                    const float2 v = fmul2(make_float2(p[2 * y], p[2 * y + 1]), both(tp));
+                    w[y] = Elem<T>::pack(v.x, v.y);
+                }
                 tc_st16(tmem + lanes + kColA + 16u * hc, w);
                 tc_wait_st();
                 tc_fence_before();
@@ -515,22 +545,19 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                 for (int x = tid; x < (int)KB / 16; x += kLtPass) {
                     const int r = (x >> 3) & 127;
                     const float w = dec[3 * C + r] * pk;
-                    const uint4 kv = lds128(k + 16u * x);
+                    const uint4 kv = r < n ? lds128(k + 16u * x) : make_uint4(0, 0, 0, 0);
                     const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w};
+                    const float2 less = both(-1.f);
                     uint32_t p0[4], p1[4], p2[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        float2 f = Elem<T>::unpack(kw[y]);
-                        f.x = r < n ? f.x * w : 0.f;
-                        f.y = r < n ? f.y * w : 0.f;
+                        float2 f = fmul2(Elem<T>::unpack(kw[y]), both(w));
                         p0[y] = Elem<T>::pack(f.x, f.y);
-                        const float2 u = Elem<T>::unpack(p0[y]);
-                        f.x -= u.x;
-                        f.y -= u.y;
+                        f = ffma2(Elem<T>::unpack(p0[y]), less, f);      // exact: what the part left
                         p1[y] = Elem<T>::pack(f.x, f.y);
                         if (!kHalf16) {
-                            const float2 v = Elem<T>::unpack(p1[y]);
-                            p2[y] = Elem<T>::pack(f.x - v.x, f.y - v.y);
+                            f = ffma2(Elem<T>::unpack(p1[y]), less, f);
+                            p2[y] = Elem<T>::pack(f.x, f.y);
                         }
                     }
                     sts128(k + 16u * x, make_uint4(p0[0], p0[1], p0[2], p0[3]));
@@ -562,12 +589,20 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                         float v[8];
                         const float4 f0 = *reinterpret_cast<const float4*>(colf + 32 * hc + 8 * y);
                         const float4 f4 = *reinterpret_cast<const float4*>(colf + 32 * hc + 8 * y + 4);
-                        const float cf[8] = {f0.x, f0.y, f0.z, f0.w, f4.x, f4.y, f4.z, f4.w};
+                        const float2 cf[4] = {make_float2(f0.x, f0.y), make_float2(f0.z, f0.w), make_float2(f4.x, f4.y),
+                                              make_float2(f4.z, f4.w)};
 #pragma unroll
-                        for (int z = 0; z < 8; ++z) {
-                            v[z] = vi[8 * y + z] * cf[z] * eb + vo[8 * y + z] * rowf;
-                            if (bad && badc[bad_now + 32 * hc + 8 * y + z] <= row) v[z] = __int_as_float(0x7FFFFFFF);
+                        for (int z = 0; z < 4; ++z) {
+                            const int at = 8 * y + 2 * z;
+                            const float2 u = fmul2(make_float2(vi[at], vi[at + 1]), cf[z]);
+                            const float2 t = ffma2(u, both(eb), fmul2(make_float2(vo[at], vo[at + 1]), both(rowf)));
+                            v[2 * z] = t.x;
+                            v[2 * z + 1] = t.y;
                         }
+                        if (bad)
+#pragma unroll
+                            for (int z = 0; z < 8; ++z)
+                                if (badc[bad_now + 32 * hc + 8 * y + z] <= row) v[z] = __int_as_float(0x7FFFFFFF);
                         const int ch = 4 * hc + y;
                         sts128(sS + (uint32_t)(row * 256 + (((ch & 8) | ((ch ^ row) & 7)) << 4)), pack8<T>(v));
                     }
