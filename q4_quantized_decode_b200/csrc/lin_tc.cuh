@@ -14,13 +14,14 @@
 //   warp 16    one thread issues the products
 //   warp 17    one thread loads Q, K and V by tensor map, K a chunk ahead
 //   warp 18    sums of the log decays, a chunk ahead
-// What bounds it: the passes, about 5 instructions for each of 5 x 16384 values
-// of a chunk.  Of a chunk's 5.2 us (with 40 heads of 128 x 128, f16) the
-// state's pass takes 0.8, the values' 0.4, the scores' 1.0, the keys' 0.7, the
-// outputs' 1.4 and the keys' maximum 0.4; the products alone are 2560 cycles.
-// Measured: three prompts of up to 16384 tokens 685 us, one of 8192 211 us (102
-// TFLOP/s of the recurrence's products).  Passes shared with four more warps
-// (705 us) and e^{-b_j} taken out of the scores' pass (686) gained nothing.
+//   warp 19    the largest key of a chunk, a chunk ahead
+// What bounds it: the passes between the products, 16 warps one after the
+// other over 5 x 16384 values of a chunk: of its 4.4 us (f16, 40 heads of 128 x
+// 128) the keys take 0.7, the state 1.0, the scores 0.9, the values 0.3, the
+// outputs 0.8, and barriers and latencies the rest; the products alone are 2560
+// cycles.  Outputs of whole chunks leave by tensor map (with stores by the
+// passes: 9 % more).  Measured: three prompts of up to 16384 tokens 568 us (bf16
+// 606), one of 8192 187 us, 115 TFLOP/s of the recurrence's products.
 //
 // Number formats.  State and sums are in 32 bits.  The split keys carry 22
 // (binary16: two parts) or 24 (bfloat16: three) significant bits into the
@@ -62,7 +63,7 @@ __host__ __device__ constexpr int lt_smem(int dk, bool out) {
 struct LinTcArgs {
     LinSegArgs g;
     uint32_t idesc_a, idesc_i, idesc_o, idesc_s;     // of the four products
-    CUtensorMap qmap, kmap, vmap;                    // [row][head][element], boxes of 64 elements x 128 rows
+    CUtensorMap qmap, kmap, vmap, omap;              // [row][head][element], boxes of 64 elements x 128 rows
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -71,6 +72,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
                  ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
                  : "memory");
 }
+
+// A box from shared memory, in this thread's next group of stores.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// This thread's stores have left shared memory; have been written.
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Sums of a chunk's log decays by one warp, four tokens a lane, in units of
 // log2: [128] b_i high parts, [128] low parts, [128] e^{b_i}, [128] e^{b_C -
@@ -121,6 +132,7 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 template <typename T, int DK, bool OUT>
 __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_constant__ LinTcArgs ta) {
     constexpr bool kHalf16 = Elem<T>::kExpMask == Elem<__half>::kExpMask;
+    constexpr bool kAhead = OUT && kHalf16;              // the largest keys come from warp 19
     constexpr int C = kLtTokens;
     constexpr uint32_t KB = lt_kbytes(DK);
     constexpr int CW = DK / kLtParts;                    // state columns of a thread: 32 or 16
@@ -139,7 +151,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     float* sy = sx + kLtParts * 128;
     float* colf = sy + kLtParts * 128;                              // [128] scale of a value column of the state's operand
     volatile int* badc = reinterpret_cast<volatile int*>(colf + 128);   // [2][128] first token with a bad value, or 128
-    uint32_t* sMax = reinterpret_cast<uint32_t*>(colf + 384);           // [16] largest |k|
+    uint32_t* sMax = reinterpret_cast<uint32_t*>(colf + 384);           // [16] largest |k|: of two chunks, or of the warps' parts
     volatile int* any_bad = reinterpret_cast<volatile int*>(sMax + 16); // [2]
     volatile int* abort_flag = any_bad + 2;
     volatile int* never = any_bad + 3;
@@ -147,13 +159,14 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     uint64_t* bars = reinterpret_cast<uint64_t*>(sMax + 32);
     uint64_t *kfull = bars, *qfull = bars + 2, *vfull = bars + 3, *dfull = bars + 4, *dfree = bars + 6, *qkdone = bars + 8,
              *qfree = bars + 9, *odone = bars + 10, *kvdone = bars + 11, *sready = bars + 12, *pready = bars + 13,
-             *kready = bars + 14, *oread = bars + 15, *idle = bars + 16;
+             *kready = bars + 14, *oread = bars + 15, *idle = bars + 16, *kmax = bars + 17;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(kfull + i, 1);
             mbar_init(dfull + i, 1);
+            mbar_init(kmax + i, 1);
             mbar_init(dfree + i, kLtPass / 32);
             any_bad[i] = 0;
         }
@@ -255,6 +268,35 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         }
         if (!ok) give_up();
         if (!OUT && work && lane == 0 && blockIdx.y == 0) *seg_decay(g, s, h, seg) = expf((float)total);
+    } else if (warp == 19) {
+        // ---- the chunks' largest keys, a chunk ahead (with OUT: without the
+        // outputs a chunk is too short for one warp, and the passes look) ----
+        if (kAhead) {
+            bool ok = true;
+            for (int c = 0; c < nc; ++c) {
+                ok = __all_sync(0xFFFFFFFFu, tc_wait_long(kfull + (c & 1), (c >> 1) & 1, abort_flag));
+                if (!ok) break;
+                const int n = (int)min((int64_t)C, t1 - t0 - (int64_t)c * C);
+                uint32_t m = 0;
+#pragma unroll 1
+                for (int x0 = lane; x0 < (int)KB / 16; x0 += 512) {
+                    uint4 v[16];
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) v[y] = lds128(sK + (c & 1) * KB + 16u * (x0 + 32 * y));
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) m = __vmaxu2(m, (((x0 + 32 * y) >> 3) & 127) < n ? max_abs8(0u, v[y]) : 0u);
+                }
+                for (int x = 16; x; x >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+                // The passes have read the last but one: its keys were freed
+                // after them.
+                if (lane == 0) {
+                    sMax[c & 1] = max(m & 0xFFFFu, m >> 16);
+                    mbar_arrive(kmax + (c & 1));
+                }
+                __syncwarp();
+            }
+            if (!ok) give_up();
+        }
     } else if (warp == 16) {
         // ---- products ----
         if (lane == 0) {
@@ -327,7 +369,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         auto store_state = [&](const uint32_t (&v)[CW]) {
             if constexpr (CW == 32) tc_st32(tS, v);
             else tc_st16(tS, v);
-            tc_wait_st();
         };
         // The first state.
         {
@@ -336,6 +377,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             for (int y = 0; y < CW; ++y)
                 v[y] = from && real && hc * CW + y < a.k_dim ? __float_as_uint(from[(int64_t)(hc * CW + y) * a.v_dim]) : 0u;
             store_state(v);
+            tc_wait_st();
             if (nc == 0 && to && real)
 #pragma unroll
                 for (int y = 0; y < CW; ++y)
@@ -362,23 +404,23 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             const int bad_now = 128 * (c & 1), bad_then = 128 * ((c & 1) ^ 1);
 
             // The chunk's largest key, and the common end after a wait that gave up.
-            wait(kfull + (c & 1), c >> 1);
-            if (kHalf16) {
+            wait(kAhead ? kmax + (c & 1) : kfull + (c & 1), c >> 1);
+            if (kHalf16 && !kAhead) {
                 uint32_t m = 0;
 #pragma unroll 4
                 for (int x = tid; x < (int)KB / 16; x += kLtPass)
                     if (((x >> 3) & 127) < n) m = max_abs8(m, lds128(k + 16u * x));
                 for (int x = 16; x; x >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-                if (lane == 0) sMax[warp] = m;
+                if (lane == 0) sMax[warp] = max(m & 0xFFFFu, m >> 16);
             }
             wait(dfull + (c & 1), c >> 1);
             if (!all_of<kLtPass>(ok)) break;
             int sk = 0;
             if (kHalf16) {
-                uint32_t m = sMax[0];
+                uint32_t top = *reinterpret_cast<volatile uint32_t*>(sMax + (kAhead ? c & 1 : 0));
+                if (!kAhead)
 #pragma unroll
-                for (int y = 1; y < kLtPass / 32; ++y) m = __vmaxu2(m, sMax[y]);
-                const uint32_t top = max(m & 0xFFFFu, m >> 16);
+                    for (int y = 1; y < kLtPass / 32; ++y) top = max(top, sMax[y]);
                 // The largest to [2^14, 2^15); with infinities or NaN, what suits any finite key.
                 sk = top >= Elem<__half>::kExpMask ? -2
                                                    : to_2_14(__half2float(__ushort_as_half((unsigned short)top)), 24);
@@ -402,6 +444,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                 for (int y = 0; y < CW; y += 2) m = max_abs(m, pair(y));
                 sx[128 * hc + row] = m;
             }
+            if (OUT && tid == 0) tma_store_read();           // the operand's place is free of the last outputs
             bar();
             if (OUT && kHalf16) {
                 float m = sx[row];
@@ -438,14 +481,17 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                 sv[y + 1] = __float_as_uint(v.y);
             }
             store_state(sv);
+            tc_wait_st();
             tc_fence_before();
             E = sk;
             tell(sready);
 
             // Values: rows behind the chunk's tokens to zero, and those that
-            // are not finite, which are remembered.
-            wait(vfull, c);
-            {
+            // are not finite, which are remembered.  They come after the last
+            // chunk's products, in bfloat16 with the queries, so there is time
+            // for the scores first where the queries are early.
+            auto look_over = [&]() {
+                wait(vfull, c);
                 constexpr int N = (int)(2 * kLtHalf / 16) / kLtPass;
                 uint32_t top = 0;
 #pragma unroll
@@ -471,7 +517,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                     }
                     fence_proxy_async_smem();
                 }
-            }
+            };
+            if (!kHalf16 && OUT) look_over();
 
             float rowf = 1.f;
             if (OUT) {
@@ -532,6 +579,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                     w[y] = Elem<T>::pack(v.x, v.y);
                 }
                 tc_st16(tmem + lanes + kColA + 16u * hc, w);
+            }
+
+            if (kHalf16 || !OUT) look_over();
+            if (OUT) {
                 tc_wait_st();
                 tc_fence_before();
                 tell(pready);
@@ -539,6 +590,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             }
 
             // The decayed keys in parts, the first in the keys' own place.
+            if (kAhead) wait(kfull + (c & 1), c >> 1);
             {
                 const float pk = exp2i(sk);
 #pragma unroll 2
@@ -604,19 +656,33 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                             for (int z = 0; z < 8; ++z)
                                 if (badc[bad_now + 32 * hc + 8 * y + z] <= row) v[z] = __int_as_float(0x7FFFFFFF);
                         const int ch = 4 * hc + y;
-                        sts128(sS + (uint32_t)(row * 256 + (((ch & 8) | ((ch ^ row) & 7)) << 4)), pack8<T>(v));
+                        sts128(sS + (uint32_t)(ch >> 3) * kLtHalf + (uint32_t)(row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
+                               pack8<T>(v));
                     }
                 }
-                bar();
+                if (n == C) {                            // a whole box
+                    fence_proxy_async_smem();
+                    bar();
+                    if (tid == 0) {
+                        for (int i = 0; i < 2; ++i)
+                            if (c0 + 64 * i < a.v_dim) tma_store_3d(&ta.omap, sS + i * kLtHalf, c0 + 64 * i, h, (int)t);
+                        tma_store_commit();
+                    }
+                } else {
+                    bar();
 #pragma unroll
-                for (int x = 0; x < C * 16 / kLtPass; ++x) {
-                    const int r = (tid >> 4) + x * (kLtPass / 16), ch = tid & 15;
-                    const uint4 v = lds128(sS + (uint32_t)(r * 256 + (((ch & 8) | ((ch ^ r) & 7)) << 4)));
-                    if (r < n && c0 + 8 * ch < a.v_dim) *reinterpret_cast<uint4*>(ob + (t + r) * a.o_stride + 8 * ch) = v;
+                    for (int x = 0; x < C * 16 / kLtPass; ++x) {
+                        const int r = (tid >> 4) + x * (kLtPass / 16), ch = tid & 15;
+                        const uint4 v =
+                            lds128(sS + (uint32_t)(ch >> 3) * kLtHalf + (uint32_t)(r * 128 + (((ch & 7) ^ (r & 7)) << 4)));
+                        if (r < n && c0 + 8 * ch < a.v_dim) *reinterpret_cast<uint4*>(ob + (t + r) * a.o_stride + 8 * ch) = v;
+                    }
                 }
             }
             tell(dfree + (c & 1));
         }
+
+        if (OUT && tid == 0) tma_store_done();
 
         // The last state.
         if (ok && nc > 0 && to) {

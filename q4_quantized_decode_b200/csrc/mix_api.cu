@@ -492,7 +492,8 @@ cudaError_t lin_prompt_launch(const q4::LinArgs& a, int64_t qk_heads, int dtype,
     const bool tc = a.k_dim <= 128 && a.rows > 0 &&
                     row_map(&ta.qmap, a.q, dtype, a.k_dim, qk_heads, a.rows, a.q_stride) &&
                     row_map(&ta.kmap, a.k, dtype, a.k_dim, qk_heads, a.rows, a.k_stride) &&
-                    row_map(&ta.vmap, a.v, dtype, a.v_dim, a.v_heads, a.rows, a.v_stride);
+                    row_map(&ta.vmap, a.v, dtype, a.v_dim, a.v_heads, a.rows, a.v_stride) &&
+                    row_map(&ta.omap, a.out, dtype, a.v_dim, a.v_heads, a.rows, a.o_stride);
     g.tokens = tc ? q4::kLtTokens : q4::kLcTokens;
     const int64_t slices = tc ? (a.v_dim + 127) / 128 : (a.v_dim + 63) / 64;
     const int64_t ctas = (int64_t)a.n_seqs * a.v_heads * slices;

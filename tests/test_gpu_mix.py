@@ -729,6 +729,24 @@ def test_linear_decay_of_minus_infinity_clears(eng):
         c.check(out, state)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dv", [8, 72, 128, 200])
+def test_linear_prompts_write_their_rows_only(eng, dtype, dv):
+    """Whole chunks of outputs leave in boxes: a strided output with columns
+    around the heads and rows before, between and behind the sequences keeps
+    what it had there."""
+    c = LinearCase([300, 0, 128, 131], 1, 2, 64, dv, dtype, seed=dv)
+    rows, w = c.rows, 2 * dv
+    wide = torch.full((rows + 150, w + 24), 3.0, dtype=dtype, device=DEV)
+    out = wide[:, 16:16 + w].unflatten(1, (2, dv))
+    pad = lambda x: torch.cat((x, x.new_full((150,) + x.shape[1:], float("nan"))))  # noqa: E731
+    got, state = eng.linattn(pad(c.gq), pad(c.gk), pad(c.gv), pad(c.gg), c.start, c.state.to(DEV),
+                             slots=c.slots.to(DEV), out=out, max_new=300)
+    assert eng.sync_status() == q4.Q4_OK
+    c.check(got[:rows], state)
+    assert (wide[rows:] == 3.0).all() and (wide[:, :16] == 3.0).all() and (wide[:, 16 + w:] == 3.0).all()
+
+
 def test_linear_zero_state_and_out_of_place(eng):
     for new in ([1, 2], [100, 30]):
         c = LinearCase(new, 1, 2, 64, 128, torch.bfloat16, seed=23)
