@@ -533,14 +533,14 @@ class Q4Gemv:
             return _raw_stream(self.device)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    def _new(self, shape, dtype, stream):
-        """An output, from the pool of the stream that writes it."""
+    def _new(self, like, shape, stream):
+        """An output of the type and device of `like`, from the pool of the stream that writes it."""
         if stream is None:
-            return _torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
+            return like.new_empty(shape)
         if not hasattr(stream, "cuda_stream"):
             stream = _torch.cuda.ExternalStream(int(stream), device=self.device)
         with _torch.cuda.stream(stream):
-            return _torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
+            return like.new_empty(shape)
 
     def rope_freqs(self, rot: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0,
                    trained: float = 0.0, lo: float = 1.0, hi: float = 32.0):
@@ -573,7 +573,7 @@ class Q4Gemv:
             if n != rows or d != dim:
                 _want("q", (n, hq, d), (rows, hq, dim))
             if q_out is None:
-                q_out = self._new(q.shape, q.dtype, stream)
+                q_out = self._new(q, q.shape, stream)
             n, m, d, qos = _rows(q_out, "q_out", dt, dev)
             if n != rows or m != hq or d != dim:
                 _want("q_out", (n, m, d), (rows, hq, dim))
@@ -602,7 +602,7 @@ class Q4Gemv:
         if d != dim:
             _want("q", (rows, hq, d), (rows, hq, dim))
         if out is None:
-            out = self._new(q.shape, q.dtype, stream)
+            out = self._new(q, q.shape, stream)
         n, m, d, os_ = _rows(out, "out", dt, dev)
         if n != rows or m != hq or d != dim:
             _want("out", (n, m, d), (rows, hq, dim))
@@ -635,7 +635,7 @@ class Q4Gemv:
         if n != rows:
             _want("v", (n, hv, dv), (rows, hv, dv))
         if out is None:
-            out = self._new((rows, hv, dv), dt, stream)
+            out = self._new(q, (rows, hv, dv), stream)
         n, m, d, os_ = _rows(out, "out", dt, dev)
         if n != rows or m != hv or d != dv:
             _want("out", (n, m, d), (rows, hv, dv))
@@ -691,7 +691,7 @@ class Q4Gemv:
             self._on_device(freqs.get_device())
             rope = q4gemv_rope(freqs.data_ptr(), 2 * freqs.numel(), interleaved, amp)
         if x_out is None:
-            x_out = self._new((hidden,), _torch.float16, stream)
+            x_out = self._new(x_in, (hidden,), stream)
         elif x_out.dtype is not _torch.float16 or x_out.numel() != hidden or not x_out.is_contiguous():
             raise Q4Error(Q4_ESHAPE, f"x_out: contiguous float16 [{hidden}] expected")
         self._on_device(x_out.get_device())
