@@ -76,7 +76,6 @@ struct TcAttnArgs {
     float* ws;           // [2 * gridDim.x] slots
     int* cnt;            // [gridDim.x] arrivals, zero between calls
     int min_rows;        // sequences of at most this many rows are another kernel's
-    int rows;            // of a unit
     uint32_t idesc_s, idesc_o;
     int box;             // tokens of a tensor-map box (8..128, dividing page_size), 0: no maps
     CUtensorMap kmap, vmap;   // [page][head][token][element], boxes of 64 elements x `box` tokens
@@ -89,6 +88,7 @@ struct TaSeq {
     __device__ __forceinline__ int64_t before(int64_t rt) const { return rt * c0 + c1 * (rt * (rt - 1) / 2); }
 };
 
+template <int ROWS>
 __device__ __forceinline__ TaSeq ta_seq(const TcAttnArgs& g, int s) {
     TaSeq q;
     seq_rows(g.a.batch, s, q.first, q.n);
@@ -96,11 +96,11 @@ __device__ __forceinline__ TaSeq ta_seq(const TcAttnArgs& g, int s) {
     const int64_t rows = (int64_t)q.n * g.a.group;
     q.tiles = q.c0 = q.c1 = 0;
     if (rows <= g.min_rows) return q;
-    q.tiles = (int)((rows + g.rows - 1) / g.rows);
+    q.tiles = (int)((rows + ROWS - 1) / ROWS);
     int lo, hi;
     if (g.a.causal && (g.a.window == 0 || g.a.window >= q.len)) {
-        seen_range(g.a, q.len, q.n, min(q.n - 1, (g.rows - 1) / g.a.group), lo, hi);
-        q.c1 = g.rows / g.a.group;
+        seen_range(g.a, q.len, q.n, min(q.n - 1, (ROWS - 1) / g.a.group), lo, hi);
+        q.c1 = ROWS / g.a.group;
     } else {
         seen_range(g.a, q.len, q.n, q.n - 1, lo, hi);
     }
@@ -133,6 +133,7 @@ struct TaWalk {
 };
 
 // The sequence whose units (by count, or by cost) hold place x.
+template <int ROWS>
 __device__ __forceinline__ void ta_find(const TcAttnArgs& g, int64_t x, bool by_units, int& s, int64_t& base) {
     const int lane = threadIdx.x & 31, nh = g.a.kv.n_heads, n_seqs = g.a.batch.n_seqs;
     base = 0;
@@ -140,7 +141,7 @@ __device__ __forceinline__ void ta_find(const TcAttnArgs& g, int64_t x, bool by_
     for (int c0 = 0; c0 < n_seqs; c0 += 32) {
         int64_t v = 0;
         if (c0 + lane < n_seqs) {
-            const TaSeq q = ta_seq(g, c0 + lane);
+            const TaSeq q = ta_seq<ROWS>(g, c0 + lane);
             v = (by_units ? q.tiles : q.before(q.tiles)) * nh;
         }
         int64_t p = v;
@@ -182,9 +183,10 @@ __device__ __forceinline__ void ta_unit(const TaSeq& q, int nh, int64_t x, int& 
 
 // Keys of row tile rt (the first row starts lowest, the last ends highest):
 // the first 128-key tile's first key, the tiles.
+template <int ROWS>
 __device__ __forceinline__ int ta_tiles(const TcAttnArgs& g, const TaSeq& q, int rt, int& tlo, int& thi, int& base) {
-    const int t0 = (int)div_floor((int64_t)rt * g.rows, g.a.group);
-    const int t1 = min(q.n - 1, (int)div_floor((int64_t)(rt + 1) * g.rows - 1, g.a.group));
+    const int t0 = (int)div_floor((int64_t)rt * ROWS, g.a.group);
+    const int t1 = min(q.n - 1, (int)div_floor((int64_t)(rt + 1) * ROWS - 1, g.a.group));
     int lo1, hi0;
     seen_range(g.a, q.len, q.n, t0, tlo, hi0);
     seen_range(g.a, q.len, q.n, t1, lo1, thi);
@@ -205,26 +207,28 @@ __device__ __forceinline__ int ta_snap(int T, int in, int cu) {
 
 // Moves a cut to where ta_snap puts it; sets the walk's sequence to the one
 // that holds it.
+template <int ROWS>
 __device__ __forceinline__ int64_t ta_snapped(const TcAttnArgs& g, TaWalk& w, int c) {
     if (c == 0) return 0;
     if (c >= w.runs) return w.total;
     const int64_t x = w.cut(c);
     int s, rt, hk, in, lo, hi, base;
     int64_t sb;
-    ta_find(g, x, false, s, sb);
-    const TaSeq q = ta_seq(g, s);
+    ta_find<ROWS>(g, x, false, s, sb);
+    const TaSeq q = ta_seq<ROWS>(g, s);
     ta_unit(q, g.a.kv.n_heads, x - sb, rt, hk, in);
-    const int T = ta_tiles(g, q, rt, lo, hi, base), cu = q.c0 + q.c1 * rt;
+    const int T = ta_tiles<ROWS>(g, q, rt, lo, hi, base), cu = q.c0 + q.c1 * rt;
     const int i = ta_snap(T, in, cu);
     return i == 0 ? x - in : i >= T ? x - in + cu : x;
 }
 
+template <int ROWS>
 __device__ __forceinline__ TaWalk ta_start(const TcAttnArgs& g) {
     TaWalk w;
     const int lane = threadIdx.x & 31, nh = g.a.kv.n_heads, n_seqs = g.a.batch.n_seqs;
     int64_t units = 0, cost = 0;
     for (int s = lane; s < n_seqs; s += 32) {
-        const TaSeq q = ta_seq(g, s);
+        const TaSeq q = ta_seq<ROWS>(g, s);
         units += (int64_t)q.tiles * nh;
         cost += q.before(q.tiles) * nh;
     }
@@ -244,23 +248,24 @@ __device__ __forceinline__ TaWalk ta_start(const TcAttnArgs& g) {
         const int u = c / w.k;
         w.done = u >= units;
         if (w.done) return w;
-        ta_find(g, u, true, w.s, w.seq_base);
-        w.q = ta_seq(g, w.s);
+        ta_find<ROWS>(g, u, true, w.s, w.seq_base);
+        w.q = ta_seq<ROWS>(g, w.s);
         w.b = u - w.seq_base;                 // the unit within the sequence
         return w;
     }
     w.runs = (int)gridDim.x;
     w.ratio = (double)cost / (double)w.runs;
-    w.b0 = w.b = ta_snapped(g, w, c);
-    w.b1 = ta_snapped(g, w, c + 1);
+    w.b0 = w.b = ta_snapped<ROWS>(g, w, c);
+    w.b1 = ta_snapped<ROWS>(g, w, c + 1);
     w.done = w.b >= w.b1;
     if (w.done) return w;
-    ta_find(g, w.b, false, w.s, w.seq_base);
-    w.q = ta_seq(g, w.s);
+    ta_find<ROWS>(g, w.b, false, w.s, w.seq_base);
+    w.q = ta_seq<ROWS>(g, w.s);
     return w;
 }
 
 // The next part of this CTA's run; e.more = 0 at its end.
+template <int ROWS>
 __device__ __forceinline__ void ta_next(const TcAttnArgs& g, TaWalk& w, TaSeg& e) {
     e.more = 0;
     const int nh = g.a.kv.n_heads;
@@ -270,7 +275,7 @@ __device__ __forceinline__ void ta_next(const TcAttnArgs& g, TaWalk& w, TaSeg& e
         w.done = true;
         rt = (int)div_floor(w.b, nh);
         hk = (int)(w.b - (int64_t)rt * nh);
-        const int T = ta_tiles(g, w.q, rt, e.tlo, e.thi, base);
+        const int T = ta_tiles<ROWS>(g, w.q, rt, e.tlo, e.thi, base);
         // As many pieces as leave a piece about as many tiles as there are
         // pieces to join.
         int k = 1;
@@ -290,13 +295,13 @@ __device__ __forceinline__ void ta_next(const TcAttnArgs& g, TaWalk& w, TaSeg& e
         }
         while (w.b >= w.seq_base + w.q.before(w.q.tiles) * nh && w.s + 1 < g.a.batch.n_seqs) {
             w.seq_base += w.q.before(w.q.tiles) * nh;
-            w.q = ta_seq(g, ++w.s);
+            w.q = ta_seq<ROWS>(g, ++w.s);
         }
         ta_unit(w.q, nh, w.b - w.seq_base, rt, hk, in);
         const int cu = w.q.c0 + w.q.c1 * rt;
         const int64_t ub = w.b - in, ue = ub + cu;
         const int64_t stop = w.b1 < ue ? w.b1 : ue;
-        const int T = ta_tiles(g, w.q, rt, e.tlo, e.thi, base);
+        const int T = ta_tiles<ROWS>(g, w.q, rt, e.tlo, e.thi, base);
         i0 = in == 0 ? 0 : (int)div_floor((int64_t)T * in, cu);
         i1 = stop == ue ? T : (int)div_floor((int64_t)T * (stop - ub), cu);
         // The runs that begin inside the unit are consecutive; the run before
@@ -317,7 +322,7 @@ __device__ __forceinline__ void ta_next(const TcAttnArgs& g, TaWalk& w, TaSeg& e
         e.c_lo = inside ? c_first - 1 : (int)blockIdx.x;
         e.slot = 2 * (int)blockIdx.x + (w.b == w.b0 ? 0 : 1);
         e.slot0 = e.slot;
-        if (inside) e.slot0 = 2 * e.c_lo + (ta_snapped(g, w, e.c_lo) < ub ? 1 : 0);
+        if (inside) e.slot0 = 2 * e.c_lo + (ta_snapped<ROWS>(g, w, e.c_lo) < ub ? 1 : 0);
         w.b = stop;
     }
     e.more = 1;
@@ -326,9 +331,9 @@ __device__ __forceinline__ void ta_next(const TcAttnArgs& g, TaWalk& w, TaSeg& e
     e.len = w.q.len;
     e.n = w.q.n;
     e.first = w.q.first;
-    e.n_rows = (int)min((int64_t)g.rows, (int64_t)w.q.n * g.a.group - (int64_t)rt * g.rows);
-    e.t0 = (int)div_floor((int64_t)rt * g.rows, g.a.group);
-    e.g0 = (int)((int64_t)rt * g.rows - (int64_t)e.t0 * g.a.group);
+    e.n_rows = (int)min((int64_t)ROWS, (int64_t)w.q.n * g.a.group - (int64_t)rt * ROWS);
+    e.t0 = (int)div_floor((int64_t)rt * ROWS, g.a.group);
+    e.g0 = (int)((int64_t)rt * ROWS - (int64_t)e.t0 * g.a.group);
     e.j0 = base + i0 * kTaKeys;
     e.nt = i1 - i0;
 }
@@ -603,10 +608,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) attn_tc_kernel(const __grid_con
         if (!ok) give_up();
         } else {
             // ---- the walk over this CTA's parts ----
-            TaWalk w = ta_start(g);
+            TaWalk w = ta_start<ROWS>(g);
             for (uint32_t n = 0;; ++n) {
                 TaSeg e;
-                ta_next(g, w, e);
+                ta_next<ROWS>(g, w, e);
                 if (n >= kTaSegs && !__all_sync(0xFFFFFFFFu, tc_wait_long(pempty_seg + n % kTaSegs, (n / kTaSegs - 1) & 1,
                                                                      abort_flag))) {
                     give_up();

@@ -430,7 +430,6 @@ int q4gemv_attn_paged(q4gemv_t h, const q4gemv_kv* kv, int64_t rows, int64_t n_s
         g.cnt = cx.attn_cnt;
         g.min_rows = few ? limit : 0;
         const int dp = split_dp(kv->head_dim);
-        g.rows = q4::ta_rows(dp);
         // Boxes of the largest power of two of tokens that divides a page, up
         // to a tile; under 8 they would be more than the 16-byte copies' work.
         g.box = (int)std::min<int64_t>(kv->page_size & -kv->page_size, q4::kTaKeys);
