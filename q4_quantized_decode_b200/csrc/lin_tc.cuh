@@ -16,11 +16,11 @@
 //   warp 18    sums of the log decays, a chunk ahead
 //   warp 19    the largest key of a chunk, a chunk ahead
 // What bounds it: the passes between the products, 16 warps one after the
-// other over 5 x 16384 values of a chunk: of its 4.4 us (f16, 40 heads of 128 x
+// other over 5 x 16384 values of a chunk: of its 4.5 us (f16, 40 heads of 128 x
 // 128) the keys take 0.7, the state 1.0, the scores 0.9, the values 0.3, the
 // outputs 0.8, and barriers and latencies the rest; the products alone are 2560
 // cycles.  Outputs of whole chunks leave by tensor map (with stores by the
-// passes: 9 % more).  Measured: three prompts of up to 16384 tokens 568 us (bf16
+// passes: 9 % more).  Measured: three prompts of up to 16384 tokens 576 us (bf16
 // 606), one of 8192 187 us, 115 TFLOP/s of the recurrence's products.
 //
 // Number formats.  State and sums are in 32 bits.  The split keys carry 22
