@@ -579,7 +579,9 @@ typedef struct {
  * writes state_out (of the sequences' slots only; a sequence without new
  * tokens copies its state).  A sequence whose slot is outside [0, n_slots) is
  * left out, its rows unwritten (Q4_EINDEX).  max_new as in
- * q4gemv_attn_paged. */
+ * q4gemv_attn_paged.  States are good up to magnitudes of 2^80 (many new tokens
+ * are run in chunks that scale them by powers of two); an infinity in q, k or v
+ * may come out as NaN wherever the formula takes it, and nowhere else. */
 Q4GEMV_API int q4gemv_linattn(q4gemv_t h, const q4gemv_linattn_args* args, int64_t rows,
                               int64_t n_seqs, const int32_t* start, int64_t max_new,
                               q4gemv_stream_t stream);
@@ -614,7 +616,8 @@ typedef struct {
  *   x_in, x_out : device, hidden binary16 (x_out may alias x_in)
  * Launches its kernels on `stream` (4 products and 1 or 2 mixer kernels a
  * layer), so it may be captured into a graph and replayed token by token; the
- * first call with larger sizes must come outside a capture.  Arguments of all
+ * first call with larger sizes allocates (it waits for the device) and must
+ * come outside a capture.  Arguments of all
  * layers are checked before anything is launched: errors of the parts it runs;
  * Q4_ESHAPE if q_heads does not divide hidden, kv_heads does not
  * divide q_heads, or a layer's cache has other heads. */
